@@ -456,6 +456,116 @@ int moe_combine_s2f6(const int8_t* codes, const uint8_t* e8m0, int64_t M, int64_
 int pmn_check_indices(const int64_t* offsets, int G, int64_t M, const int32_t* gather, int64_t n_gather,
                       int64_t src_rows, uint32_t* result, pmn_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------ */
+/* Around the routed experts: the norm before them, the shared (dense) expert beside them and   */
+/* the update of the weights after them.                                                        */
+/* ------------------------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm of x bf16 [rows x cols] with the residual's addition:
+ *   z = x + residual (fp32), s = 1 / sqrt(mean(z^2) + eps) per row, y = z s gamma.
+ * residual: NULL (z = x; z_out is not used), or [rows x cols] of res_dtype (PMN_DTYPE_*), and then
+ *   z_out, of the same type, receives z (it may be residual itself). y is computed from the fp32 z.
+ * gamma: fp32 [cols]. Outputs, each nullable but at least one of y and codes given: y bf16
+ *   [rows x cols]; codes uint8 [rows x cols] and e8m0 uint8 [rows x cols/32], the row-wise MXFP8 form
+ *   of the fp32 y (scale rule and rounding to nearest even as mxfp8_quantize; a NaN or infinite y
+ *   has a NaN code, 0x7F or 0xFF); rstd fp32 [rows], s for the backward.
+ * cols % 8 == 0 (with codes: cols % 32 == 0), cols <= 32768, rows < 2^31 (PMN_ESHAPE); eps >= 0
+ * (PMN_EINVAL); every pointer 16-byte aligned but e8m0 (any) and rstd (4) (PMN_EALIGN).
+ */
+int rmsnorm_residual_fwd(const void* x, const void* residual, int res_dtype, const float* gamma, float eps,
+                         int64_t rows, int64_t cols, void* z_out, void* y, uint8_t* codes, uint8_t* e8m0,
+                         float* rstd, pmn_stream_t stream);
+
+/*
+ * Its backward, from the saved z [rows x cols] (z_out of the forward, or x where there was no
+ * residual) and rstd. dy [rows x cols] of dy_dtype is the gradient of y; with xh = z rstd:
+ *   dz = rstd (dy gamma - xh mean(dy gamma xh)) + dres    in z's type, z_dtype
+ *   dgamma[c] = sum over rows of dy xh                     fp32 [cols]
+ * dz is the gradient of x and of the residual alike. dres: NULL, or the gradient that reaches z_out
+ * along the residual stream, of z_dtype (dz may be dres itself). rows == 0 sets dgamma to zero.
+ * Sizes and alignment as the forward (cols % 8 == 0). Workspace (16-byte aligned, at least
+ * rmsnorm_residual_bwd_workspace_size(rows, cols) bytes, PMN_EWORKSPACE) holds partial sums of dgamma.
+ */
+size_t rmsnorm_residual_bwd_workspace_size(int64_t rows, int64_t cols);
+int rmsnorm_residual_bwd(const void* dy, int dy_dtype, const void* z, int z_dtype, const float* gamma,
+                         const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dz, float* dgamma,
+                         void* workspace, size_t workspace_bytes, pmn_stream_t stream);
+
+/*
+ * Dense gated feed-forward block (the shared expert), bf16 operands and fp32 accumulation:
+ *   [h1 | h3] = x w13^T,  a = silu(h1) h3,  y = a w2^T + add
+ * x bf16 [M x H]; w13 bf16 [2F x H] (rows 0 .. F-1 w1, F .. 2F-1 w3); w2 bf16 [H x F]; add: NULL, or
+ * bf16 [M x H] (the routed experts' sum; it may be y itself); h13_out: NULL, or bf16 [M x 2F], h1 | h3
+ * for the backward; y bf16 [M x H]. a is rounded to bf16 for the second product.
+ * H % 8 == 0, F % 8 == 0, M >= 0 (PMN_ESHAPE); pointers 16-byte aligned (PMN_EALIGN). Workspace
+ * (16-byte aligned, at least swiglu_ffn_fwd_workspace_size() bytes, PMN_EWORKSPACE).
+ */
+size_t swiglu_ffn_fwd_workspace_size(int64_t M, int64_t H, int64_t F);
+int swiglu_ffn_fwd(const void* x, const void* w13, const void* w2, const void* add, int64_t M, int64_t H,
+                   int64_t F, void* h13_out, void* y, void* workspace, size_t workspace_bytes,
+                   pmn_stream_t stream);
+
+/*
+ * Its backward from dy bf16 [M x H] and the saved h13 (the gradient of add is dy):
+ *   da = dy w2, dh1 = da h3 silu'(h1), dh3 = da silu(h1), a = silu(h1) h3
+ *   PMN_BWD_DGRAD: dx bf16 [M x H] = [dh1 | dh3] w13
+ *   PMN_BWD_WGRAD: dw13 [2F x H] = [dh1 | dh3]^T x, dw2 [H x F] = dy^T a, of dw_dtype (PMN_DTYPE_*)
+ * flags: DGRAD, WGRAD or both (PMN_EINVAL otherwise). dh1, dh3 and a are rounded to bf16 for the
+ * products; the sums are fp32. M == 0 writes zero weight gradients. Sizes, alignment and workspace as
+ * the forward (swiglu_ffn_bwd_workspace_size).
+ */
+size_t swiglu_ffn_bwd_workspace_size(int64_t M, int64_t H, int64_t F);
+int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w2, const void* h13, int64_t M,
+                   int64_t H, int64_t F, int flags, void* dx, void* dw13, void* dw2, int dw_dtype,
+                   void* workspace, size_t workspace_bytes, pmn_stream_t stream);
+
+/*
+ * AdamW over many tensors at once: fp32 weights, their bf16 copy for the quantizers, and moments in
+ * fp32 or in 8 bits. Per value, with g' = grad_scale * grad and t = step (>= 1):
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   param = param (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *   copy = bf16(param)
+ * state_bits 32: m, v fp32 [n]. state_bits 8: m and v uint8 [n] with m_e8m0, v_e8m0 uint8
+ * [ceil(n / 32)], MXFP8 over runs of 32 values of m and of sqrt(v) (zero bytes are zero moments),
+ * rounded stochastically as the requant rounds: value i of tensor j of the list draws index i under
+ * seed + step and stream rng_stream + 2 j (m) or rng_stream + 2 j + 1 (v); a root above zero gets at
+ * least the smallest code. The update uses the moments before their rounding.
+ */
+typedef struct {
+    float* param;         /* [n] */
+    const void* grad;     /* [n] of grad_dtype */
+    void* copy;           /* bf16 [n], or NULL */
+    void* m;
+    void* v;
+    uint8_t* m_e8m0;      /* state_bits 8 only */
+    uint8_t* v_e8m0;
+    int64_t n;            /* >= 0 */
+    float weight_decay;
+    int grad_dtype;       /* PMN_DTYPE_* */
+} pmn_adamw_tensor;
+
+/*
+ * The list of tensors as a table: adamw_table_build checks `tensors` (host, count of them) and writes
+ * the table into `table` (host memory, adamw_table_size bytes, 8-byte aligned) and its chunk count into
+ * *chunks (host). The caller copies the table to the device and keeps it there for as many steps
+ * as the pointers in it stay valid. Device pointers 16-byte aligned, e8m0 any (PMN_EALIGN). A tensor
+ * may not appear twice: the calls read and write every buffer once, in no order.
+ */
+size_t adamw_table_size(const pmn_adamw_tensor* tensors, int count);
+int adamw_table_build(const pmn_adamw_tensor* tensors, int count, int state_bits, void* table, size_t bytes,
+                      int64_t* chunks);
+
+/*
+ * One step over the table on the device (8-byte aligned; state_bits and chunks as built: a table of
+ * others is left alone). lr_dev, step_dev, grad_scale_dev: NULL, or device scalars read instead of
+ * lr, step and 1 (for replayed graphs, and for a clipped or unscaled gradient); a step below 1 counts
+ * as 1. 0 <= beta1, beta2 < 1, eps >= 0, lr finite, step >= 1 (PMN_EINVAL).
+ */
+int adamw_step(const void* table, int64_t chunks, int state_bits, double lr, double beta1, double beta2, double eps,
+               int64_t step, const float* lr_dev, const int64_t* step_dev, const float* grad_scale_dev,
+               uint64_t seed, uint32_t rng_stream, pmn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

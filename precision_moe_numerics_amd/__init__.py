@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import List, Optional, Union
 
 import torch
 
@@ -19,6 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpmn.so")
 
 P, I64, I32, U32, U64, SZ = C.c_void_p, C.c_int64, C.c_int, C.c_uint32, C.c_uint64, C.c_size_t
+F32, F64 = C.c_float, C.c_double
 
 _SIGS = {
     "pmn_strerror": (C.c_char_p, [I32]),
@@ -46,6 +47,16 @@ _SIGS = {
     "pmn_noalloc_scratch_bytes": (SZ, []),
     "moe_grouped_gemm_bwd_noalloc": (I32, [P, P, P, P, I64, I64, P, P, P, P, I64, P, I32, I64, I64, I64, I32, I32,
                                            U64, U32, U32, U32, P, P, P]),
+    "rmsnorm_residual_fwd": (I32, [P, P, I32, P, F32, I64, I64, P, P, P, P, P, P]),
+    "rmsnorm_residual_bwd_workspace_size": (SZ, [I64, I64]),
+    "rmsnorm_residual_bwd": (I32, [P, I32, P, I32, P, P, P, I64, I64, P, P, P, SZ, P]),
+    "swiglu_ffn_fwd_workspace_size": (SZ, [I64, I64, I64]),
+    "swiglu_ffn_fwd": (I32, [P, P, P, P, I64, I64, I64, P, P, P, SZ, P]),
+    "swiglu_ffn_bwd_workspace_size": (SZ, [I64, I64, I64]),
+    "swiglu_ffn_bwd": (I32, [P, P, P, P, P, I64, I64, I64, I32, P, P, P, I32, P, SZ, P]),
+    "adamw_table_size": (SZ, [P, I32]),
+    "adamw_table_build": (I32, [P, I32, I32, P, SZ, P]),
+    "adamw_step": (I32, [P, I64, I32, F64, F64, F64, F64, I64, P, P, P, U64, U32, P]),
     # measurement kernels (include/pmn_probe.h)
     "pmn_probe_stream": (I32, [P, P, I64, I32, I32, I32, I32, P]),
     "pmn_probe_mfma_sink_floats": (SZ, [I32, I32]),
@@ -596,6 +607,262 @@ def moe_combine_s2f6(codes: torch.Tensor, e8m0: torch.Tensor, sign_mask: int, sl
     _check(_lib.moe_combine_s2f6(_ptr(codes), _ptr(e8m0), M, H, sign_mask & 0xFFFFFFFF, _ptr(slot_of), _ptr(gates),
                                  T, k, _ptr(out), _stream()), "moe_combine_s2f6")
     return out
+
+
+# ---- around the routed experts: the norm, the shared expert and the weight update -----------
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    _need(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bf16 or fp32")
+    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+
+
+def _one_device(**tensors):
+    """Every tensor on the current device, whose current stream the call takes."""
+    for name, t in tensors.items():
+        if t is not None:
+            if not t.is_cuda:
+                raise PmnError(f"{name} must be on the GPU")
+            if t.device.index != torch.cuda.current_device():
+                raise PmnError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+@dataclass
+class RmsNorm:
+    """Outputs of rmsnorm_residual_fwd; what was not asked for is None. y bf16; codes u8 (E4M3)
+    [rows, cols] with e8m0 u8 [rows, cols/32]; z the residual stream after the addition (None without
+    a residual); rstd fp32 [rows]."""
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    e8m0: Optional[torch.Tensor]
+    z: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+def rmsnorm_residual_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
+                         residual: Optional[torch.Tensor] = None, want_y: bool = True, want_mxfp8: bool = False,
+                         want_rstd: bool = False, z_out: Optional[torch.Tensor] = None) -> RmsNorm:
+    """RMS norm of x (+ residual), bf16 [rows, cols]; residual bf16 or fp32, z_out (optional, it may be
+    residual itself) receives the sum. want_y: the bf16 output; want_mxfp8: the row-wise MXFP8 output;
+    want_rstd: what the backward needs."""
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [rows, cols]")
+    R, Cc = x.shape
+    dev = x.device
+    _tensor(gamma, (Cc,), torch.float32, "gamma")
+    _need(want_y or want_mxfp8, "want_y or want_mxfp8 must be set")
+    _need(not want_mxfp8 or Cc % 32 == 0, "MXFP8 output needs cols to be a multiple of 32")
+    _need(residual is not None or z_out is None, "z_out needs a residual")
+    rcode = DTYPE_BF16
+    if residual is not None:
+        rcode = _dtype_code(residual, "residual")
+        _tensor(residual, (R, Cc), residual.dtype, "residual")
+        z_out = torch.empty_like(residual) if z_out is None else z_out
+        _tensor(z_out, (R, Cc), residual.dtype, "z_out")
+    _one_device(x=x, gamma=gamma, residual=residual, z_out=z_out)
+    y = torch.empty((R, Cc), dtype=torch.bfloat16, device=dev) if want_y else None
+    codes = torch.empty((R, Cc), dtype=torch.uint8, device=dev) if want_mxfp8 else None
+    e8m0 = torch.empty((R, Cc // 32), dtype=torch.uint8, device=dev) if want_mxfp8 else None
+    rstd = torch.empty((R,), dtype=torch.float32, device=dev) if want_rstd else None
+    _check(_lib.rmsnorm_residual_fwd(_ptr(x), _ptr(residual), rcode, _ptr(gamma), eps, R, Cc, _ptr(z_out), _ptr(y),
+                                     _ptr(codes), _ptr(e8m0), _ptr(rstd), _stream()), "rmsnorm_residual_fwd")
+    return RmsNorm(y, codes, e8m0, z_out, rstd)
+
+
+def rmsnorm_residual_bwd(dy: torch.Tensor, z: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
+                         dres: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         dz: Optional[torch.Tensor] = None):
+    """Backward of rmsnorm_residual_fwd: z its residual stream (x where there was no residual), dres the
+    gradient that reaches z along the stream. Returns (dz [rows, cols] of z's type, dgamma fp32 [cols])."""
+    _need(z.dim() == 2, "z must be [rows, cols]")
+    R, Cc = z.shape
+    zcode, dcode = _dtype_code(z, "z"), _dtype_code(dy, "dy")
+    _tensor(dy, (R, Cc), dy.dtype, "dy")
+    _tensor(gamma, (Cc,), torch.float32, "gamma")
+    _tensor(rstd, (R,), torch.float32, "rstd")
+    if dres is not None:
+        _tensor(dres, (R, Cc), z.dtype, "dres")
+    dz = torch.empty_like(z) if dz is None else dz
+    _tensor(dz, (R, Cc), z.dtype, "dz")
+    if workspace is None:
+        workspace = torch.empty((_lib.rmsnorm_residual_bwd_workspace_size(R, Cc),), dtype=torch.uint8, device=z.device)
+    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1, "workspace must be a 1-D uint8 tensor")
+    _one_device(dy=dy, z=z, gamma=gamma, rstd=rstd, dres=dres, dz=dz, workspace=workspace)
+    dgamma = torch.empty((Cc,), dtype=torch.float32, device=z.device)
+    _check(_lib.rmsnorm_residual_bwd(_ptr(dy), dcode, _ptr(z), zcode, _ptr(gamma), _ptr(rstd), _ptr(dres), R, Cc,
+                                     _ptr(dz), _ptr(dgamma), _ptr(workspace), workspace.numel(), _stream()),
+           "rmsnorm_residual_bwd")
+    return dz, dgamma
+
+
+def swiglu_ffn_fwd_workspace_size(M: int, H: int, F: int) -> int:
+    return _lib.swiglu_ffn_fwd_workspace_size(M, H, F)
+
+
+def swiglu_ffn_bwd_workspace_size(M: int, H: int, F: int) -> int:
+    return _lib.swiglu_ffn_bwd_workspace_size(M, H, F)
+
+
+def _ffn_weights(w13: torch.Tensor, w2: torch.Tensor, H: int) -> int:
+    _need(w2.dim() == 2 and w2.shape[0] == H, f"w2 must be bf16 [{H}, F]")
+    F = w2.shape[1]
+    _tensor(w2, (H, F), torch.bfloat16, "w2")
+    _tensor(w13, (2 * F, H), torch.bfloat16, "w13")
+    return F
+
+
+def _ffn_workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1, "workspace must be a 1-D uint8 tensor")
+    return workspace
+
+
+def swiglu_ffn_fwd(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, add: Optional[torch.Tensor] = None,
+                   save_h13: bool = False, workspace: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None):
+    """The dense gated block y = (silu(x w1^T) * (x w3^T)) w2^T (+ add), bf16: x [M, H], w13 [2F, H] (w1
+    over w3), w2 [H, F]; out may be add itself. Returns (y, h13 [M, 2F] for the backward or None)."""
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [M, H]")
+    M, H = x.shape
+    F = _ffn_weights(w13, w2, H)
+    if add is not None:
+        _tensor(add, (M, H), torch.bfloat16, "add")
+    workspace = _ffn_workspace(workspace, _lib.swiglu_ffn_fwd_workspace_size(M, H, F), x.device)
+    out = torch.empty_like(x) if out is None else out
+    _tensor(out, (M, H), torch.bfloat16, "out")
+    _one_device(x=x, w13=w13, w2=w2, add=add, out=out, workspace=workspace)
+    h13 = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=x.device) if save_h13 else None
+    _check(_lib.swiglu_ffn_fwd(_ptr(x), _ptr(w13), _ptr(w2), _ptr(add), M, H, F, _ptr(h13), _ptr(out),
+                               _ptr(workspace), workspace.numel(), _stream()), "swiglu_ffn_fwd")
+    return out, h13
+
+
+def swiglu_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h13: torch.Tensor,
+                   flags: int = BWD_DGRAD | BWD_WGRAD, dw_dtype: torch.dtype = torch.float32,
+                   workspace: Optional[torch.Tensor] = None, dw13: Optional[torch.Tensor] = None,
+                   dw2: Optional[torch.Tensor] = None):
+    """Backward of swiglu_ffn_fwd from its saved h13 (the gradient of add is dy). Returns (dx bf16 [M, H]
+    or None, dw13 [2F, H] and dw2 [H, F] of dw_dtype or None), as flags asks."""
+    _need(dy.dtype == torch.bfloat16 and dy.dim() == 2, "dy must be bf16 [M, H]")
+    M, H = dy.shape
+    F = _ffn_weights(w13, w2, H)
+    _tensor(x, (M, H), torch.bfloat16, "x")
+    _tensor(h13, (M, 2 * F), torch.bfloat16, "h13")
+    _need(dw_dtype in (torch.bfloat16, torch.float32), "dw_dtype must be bf16 or fp32")
+    workspace = _ffn_workspace(workspace, _lib.swiglu_ffn_bwd_workspace_size(M, H, F), x.device)
+    dx = torch.empty_like(x) if flags & BWD_DGRAD else None
+    if flags & BWD_WGRAD:
+        dw13 = torch.empty((2 * F, H), dtype=dw_dtype, device=x.device) if dw13 is None else dw13
+        dw2 = torch.empty((H, F), dtype=dw_dtype, device=x.device) if dw2 is None else dw2
+        _tensor(dw13, (2 * F, H), dw_dtype, "dw13")
+        _tensor(dw2, (H, F), dw_dtype, "dw2")
+    else:
+        _need(dw13 is None and dw2 is None, "dw13 and dw2 need BWD_WGRAD")
+    _one_device(dy=dy, x=x, w13=w13, w2=w2, h13=h13, dw13=dw13, dw2=dw2, workspace=workspace)
+    _check(_lib.swiglu_ffn_bwd(_ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(h13), M, H, F, flags, _ptr(dx),
+                               _ptr(dw13), _ptr(dw2), DTYPE_F32 if dw_dtype == torch.float32 else DTYPE_BF16,
+                               _ptr(workspace), workspace.numel(), _stream()), "swiglu_ffn_bwd")
+    return dx, dw13, dw2
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamWPlan: param fp32 and grad (bf16 or fp32) of n values, copy (optional) its
+    bf16 copy; moments m and v fp32, or u8 with m_e8m0 and v_e8m0 u8 [ceil(n / 32)]. Updated in place."""
+    param: torch.Tensor
+    grad: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    copy: Optional[torch.Tensor] = None
+    m_e8m0: Optional[torch.Tensor] = None
+    v_e8m0: Optional[torch.Tensor] = None
+    weight_decay: float = 0.0
+
+    @staticmethod
+    def new(param: torch.Tensor, grad: torch.Tensor, state_bits: int = 32, copy: Optional[torch.Tensor] = None,
+            weight_decay: float = 0.0) -> "AdamWTensor":
+        """With zero moments."""
+        _need(state_bits in (8, 32), "state_bits must be 8 or 32")
+        n, dev = param.numel(), param.device
+        dt = torch.uint8 if state_bits == 8 else torch.float32
+        e8 = [torch.zeros(((n + 31) // 32,), dtype=torch.uint8, device=dev) if state_bits == 8 else None for _ in "mv"]
+        return AdamWTensor(param, grad, torch.zeros((n,), dtype=dt, device=dev),
+                           torch.zeros((n,), dtype=dt, device=dev), copy, e8[0], e8[1], weight_decay)
+
+
+class _AdamWEntry(C.Structure):
+    _fields_ = [("param", P), ("grad", P), ("copy", P), ("m", P), ("v", P), ("m_e8m0", P), ("v_e8m0", P),
+                ("n", I64), ("weight_decay", F32), ("grad_dtype", I32)]
+
+
+class AdamWPlan:
+    """A list of tensors to be updated together, as a table on their device, built once and kept (with
+    the tensors) for every step. All of one state width; no tensor twice."""
+
+    def __init__(self, tensors: List[AdamWTensor]):
+        self.tensors = list(tensors)
+        _need(len(self.tensors) > 0, "an AdamWPlan needs at least one tensor")
+        dev = self.tensors[0].param.device
+        self.state_bits = 8 if self.tensors[0].m.dtype == torch.uint8 else 32
+        sdt = torch.uint8 if self.state_bits == 8 else torch.float32
+        spans = []
+        for i, t in enumerate(self.tensors):
+            n = t.param.numel()
+            name = f"tensors[{i}]"
+            _need(t.param.dtype == torch.float32, f"{name}.param must be fp32")
+            _dtype_code(t.grad, f"{name}.grad")
+            for what, v, dt, k in (("grad", t.grad, t.grad.dtype, n), ("m", t.m, sdt, n), ("v", t.v, sdt, n),
+                                   ("copy", t.copy, torch.bfloat16, n), ("m_e8m0", t.m_e8m0, torch.uint8, (n + 31) // 32),
+                                   ("v_e8m0", t.v_e8m0, torch.uint8, (n + 31) // 32)):
+                if what in ("m_e8m0", "v_e8m0") and self.state_bits == 32:
+                    _need(v is None, f"{name}.{what} belongs to states in 8 bits")
+                elif what != "copy" or v is not None:
+                    _need(v is not None and v.dtype == dt and v.numel() == k, f"{name}.{what} must hold {k} values of {dt}")
+            for what in ("param", "grad", "m", "v", "copy", "m_e8m0", "v_e8m0"):
+                v = getattr(t, what)
+                if v is not None:
+                    _need(v.device == dev, f"{name}.{what} must be on {dev}")
+                    _need(v.is_contiguous(), f"{name}.{what} must be contiguous")
+                    if v.numel():
+                        spans.append((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size(), what != "grad", f"{name}.{what}"))
+        # buffers that are written overlap no other; gradients may share memory among themselves
+        spans.sort()
+        end, owner, wend, wowner = 0, "", 0, ""
+        for lo, hi, written, name in spans:
+            _need(lo >= (end if written else wend), f"{name} overlaps {owner if written else wowner}")
+            if hi > end:
+                end, owner = hi, name
+            if written and hi > wend:
+                wend, wowner = hi, name
+        entries = (_AdamWEntry * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            entries[i] = _AdamWEntry(_ptr(t.param), _ptr(t.grad), _ptr(t.copy), _ptr(t.m), _ptr(t.v), _ptr(t.m_e8m0),
+                                     _ptr(t.v_e8m0), t.param.numel(), t.weight_decay,
+                                     _dtype_code(t.grad, f"tensors[{i}].grad"))
+        size = _lib.adamw_table_size(entries, len(entries))
+        host = torch.empty(((size + 7) // 8,), dtype=torch.int64)
+        chunks = C.c_int64(0)
+        _check(_lib.adamw_table_build(entries, len(entries), self.state_bits, host.data_ptr(), host.numel() * 8,
+                                      C.byref(chunks)), "adamw_table_build")
+        self.chunks = chunks.value
+        self.table = host.to(dev)
+
+
+def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int, torch.Tensor], beta1: float = 0.9,
+               beta2: float = 0.95, eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None, seed: int = 0,
+               rng_stream: int = 0) -> None:
+    """One AdamW step over the plan's tensors, in place. step counts from 1. lr (fp32), step (int64) and
+    grad_scale (fp32) may be device tensors of one value, read when the step runs: a captured graph
+    that is replayed needs the step there, and changes it between its replays."""
+    dev = {}
+    for name, v, dt in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            _need(v.dtype == dt and v.numel() == 1, f"{name} must be one value of {dt}")
+            dev[name] = v
+    _need(grad_scale is None or "grad_scale" in dev, "grad_scale must be a device tensor")
+    _one_device(table=plan.table, **dev)
+    _check(_lib.adamw_step(_ptr(plan.table), plan.chunks, plan.state_bits, 0.0 if "lr" in dev else lr, beta1, beta2, eps,
+                           1 if "step" in dev else step, _ptr(dev.get("lr")), _ptr(dev.get("step")),
+                           _ptr(dev.get("grad_scale")), seed, rng_stream & 0xFFFFFFFF, _stream()), "adamw_step")
 
 
 # ---- measurement kernels of include/pmn_probe.h ---------------------------------------------

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "pmn.h"
 #include "pmn_kernels.hpp"
 
@@ -205,7 +207,7 @@ const char* pmn_strerror(int s)
     }
 }
 
-int pmn_version(void) { return 100; }
+int pmn_version(void) { return 101; }
 
 int64_t pmn_padded_bound(int64_t M, int G) { return ((M + 31) & ~(int64_t)31) + 32 * (int64_t)(G > 0 ? G : 0); }
 
@@ -466,6 +468,170 @@ int moe_combine_s2f6(const int8_t* codes, const uint8_t* e8m0, int64_t M, int64_
     if (!aligned(codes, 16) || !aligned(out, 16)) return PMN_EALIGN;
     return status(pmn::launch_combine_s2f6(codes, e8m0, M, H, rht_sign_mask, slot_of, gates, T, k,
                                            static_cast<uint16_t*>(out), hs(stream)));
+}
+
+static int norm_shape(int64_t rows, int64_t cols, int64_t unit)
+{
+    return rows < 0 || rows >= ((int64_t)1 << 31) || cols <= 0 || cols > 32768 || cols % unit != 0 ? PMN_ESHAPE : PMN_OK;
+}
+
+static bool bad_dtype(int d) { return d != PMN_DTYPE_BF16 && d != PMN_DTYPE_F32; }
+
+int rmsnorm_residual_fwd(const void* x, const void* residual, int res_dtype, const float* gamma, float eps,
+                         int64_t rows, int64_t cols, void* z_out, void* y, uint8_t* codes, uint8_t* e8m0,
+                         float* rstd, pmn_stream_t stream)
+{
+    if ((residual && bad_dtype(res_dtype)) || !(eps >= 0.0f)) return PMN_EINVAL;
+    const int st = norm_shape(rows, cols, codes ? 32 : 8);
+    if (st != PMN_OK || rows == 0) return st;
+    if (!x || !gamma || (!y && !codes) || !codes != !e8m0 || (residual && !z_out)) return PMN_EINVAL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || (residual && !aligned(z_out, 16)) ||
+        !aligned(y, 16) || !aligned(codes, 16) || !aligned(rstd, 4))
+        return PMN_EALIGN;
+    return status(pmn::launch_rmsnorm_fwd(static_cast<const uint16_t*>(x), residual, res_dtype == PMN_DTYPE_F32, gamma,
+                                          eps, rows, cols, z_out, static_cast<uint16_t*>(y), codes, e8m0, rstd,
+                                          hs(stream)));
+}
+
+size_t rmsnorm_residual_bwd_workspace_size(int64_t rows, int64_t cols)
+{
+    return norm_shape(rows, cols, 8) == PMN_OK ? pmn::rmsnorm_bwd_ws_bytes(rows, cols) : 0;
+}
+
+int rmsnorm_residual_bwd(const void* dy, int dy_dtype, const void* z, int z_dtype, const float* gamma,
+                         const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dz, float* dgamma,
+                         void* workspace, size_t workspace_bytes, pmn_stream_t stream)
+{
+    if (bad_dtype(dy_dtype) || bad_dtype(z_dtype)) return PMN_EINVAL;
+    const int st = norm_shape(rows, cols, 8);
+    if (st != PMN_OK) return st;
+    if (!dgamma || (rows > 0 && (!dy || !z || !gamma || !rstd || !dz))) return PMN_EINVAL;
+    if (rows > 0 && (!workspace || workspace_bytes < pmn::rmsnorm_bwd_ws_bytes(rows, cols))) return PMN_EWORKSPACE;
+    if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(gamma, 16) || !aligned(rstd, 4) || !aligned(dres, 16) ||
+        !aligned(dz, 16) || !aligned(dgamma, 16) || (rows > 0 && !aligned(workspace, 16)))
+        return PMN_EALIGN;
+    return status(pmn::launch_rmsnorm_bwd(dy, dy_dtype == PMN_DTYPE_F32, z, z_dtype == PMN_DTYPE_F32, gamma, rstd, dres,
+                                          rows, cols, dz, dgamma, static_cast<float*>(workspace), hs(stream)));
+}
+
+// sizes whose matrices stay below 2^46 values and whose tile grids fit a launch
+static bool bad_ffn_shape(int64_t M, int64_t H, int64_t F)
+{
+    const int64_t most = (int64_t)1 << 22;
+    return M < 0 || M > most || H <= 0 || H > most || H % 8 != 0 || F <= 0 || F > most || F % 8 != 0;
+}
+
+size_t swiglu_ffn_fwd_workspace_size(int64_t M, int64_t H, int64_t F)
+{
+    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 2);
+}
+
+int swiglu_ffn_fwd(const void* x, const void* w13, const void* w2, const void* add, int64_t M, int64_t H, int64_t F,
+                   void* h13_out, void* y, void* workspace, size_t workspace_bytes, pmn_stream_t stream)
+{
+    if (bad_ffn_shape(M, H, F)) return PMN_ESHAPE;
+    if (M == 0) return PMN_OK;
+    if (!x || !w13 || !w2 || !y) return PMN_EINVAL;
+    if (!workspace || workspace_bytes < swiglu_ffn_fwd_workspace_size(M, H, F)) return PMN_EWORKSPACE;
+    if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(add, 16) || !aligned(h13_out, 16) ||
+        !aligned(y, 16) || !aligned(workspace, 16))
+        return PMN_EALIGN;
+    return status(pmn::launch_ffn_fwd(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w13),
+                                      static_cast<const uint16_t*>(w2), static_cast<const uint16_t*>(add), M, H, F,
+                                      static_cast<uint16_t*>(workspace), static_cast<uint16_t*>(h13_out),
+                                      static_cast<uint16_t*>(y), hs(stream)));
+}
+
+size_t swiglu_ffn_bwd_workspace_size(int64_t M, int64_t H, int64_t F)
+{
+    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 4) + round256((size_t)(M * F) * 2);
+}
+
+int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w2, const void* h13, int64_t M,
+                   int64_t H, int64_t F, int flags, void* dx, void* dw13, void* dw2, int dw_dtype, void* workspace,
+                   size_t workspace_bytes, pmn_stream_t stream)
+{
+    if ((flags & ~(PMN_BWD_DGRAD | PMN_BWD_WGRAD)) != 0 || flags == 0) return PMN_EINVAL;
+    const bool dgrad = flags & PMN_BWD_DGRAD, wgrad = flags & PMN_BWD_WGRAD;
+    if (wgrad && bad_dtype(dw_dtype)) return PMN_EINVAL;
+    if (bad_ffn_shape(M, H, F)) return PMN_ESHAPE;
+    if (M > 0 && (!dy || !w2 || !h13 || (dgrad && (!w13 || !dx)) || (wgrad && !x))) return PMN_EINVAL;
+    if (wgrad && (!dw13 || !dw2)) return PMN_EINVAL;
+    if (M > 0 && (!workspace || workspace_bytes < swiglu_ffn_bwd_workspace_size(M, H, F))) return PMN_EWORKSPACE;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(h13, 16) ||
+        (dgrad && !aligned(dx, 16)) || (wgrad && (!aligned(dw13, 16) || !aligned(dw2, 16))) ||
+        (M > 0 && !aligned(workspace, 16)))
+        return PMN_EALIGN;
+    if (M == 0 && !wgrad) return PMN_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    return status(pmn::launch_ffn_bwd(
+        static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w13),
+        static_cast<const uint16_t*>(w2), static_cast<const uint16_t*>(h13), M, H, F, reinterpret_cast<uint16_t*>(ws),
+        reinterpret_cast<uint16_t*>(ws + round256((size_t)(M * F) * 4)), dgrad ? static_cast<uint16_t*>(dx) : nullptr,
+        wgrad ? dw13 : nullptr, dw2, dw_dtype == PMN_DTYPE_F32, hs(stream)));
+}
+
+static int64_t adamw_chunks_of(int64_t n) { return n <= 0 ? 0 : (n + pmn::adamw_chunk() - 1) / pmn::adamw_chunk(); }
+
+size_t adamw_table_size(const pmn_adamw_tensor* tensors, int count)
+{
+    if (count < 0 || (count > 0 && !tensors)) return 0;
+    size_t b = sizeof(pmn::AdamwTable) + (size_t)count * sizeof(pmn::AdamwEntry);
+    for (int i = 0; i < count; i++) b += (size_t)adamw_chunks_of(tensors[i].n) * sizeof(pmn::AdamwChunk);
+    return b;
+}
+
+int adamw_table_build(const pmn_adamw_tensor* tensors, int count, int state_bits, void* table, size_t bytes,
+                      int64_t* chunks)
+{
+    if (state_bits != 8 && state_bits != 32) return PMN_EINVAL;
+    if (count < 0) return PMN_ESHAPE;
+    if ((count > 0 && !tensors) || !chunks) return PMN_EINVAL;
+    int64_t total = 0;
+    for (int i = 0; i < count; i++) {
+        const pmn_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > ((int64_t)1 << 40)) return PMN_ESHAPE;
+        if (bad_dtype(t.grad_dtype)) return PMN_EINVAL;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_e8m0 || !t.v_e8m0))) return PMN_EINVAL;
+        if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.copy, 16) || !aligned(t.m, 16) ||
+            !aligned(t.v, 16))
+            return PMN_EALIGN;
+        total += adamw_chunks_of(t.n);
+    }
+    if (total >= ((int64_t)1 << 31)) return PMN_ESHAPE;
+    if (!table || bytes < adamw_table_size(tensors, count)) return PMN_EWORKSPACE;
+    if (!aligned(table, 8)) return PMN_EALIGN;
+    pmn::AdamwTable* head = static_cast<pmn::AdamwTable*>(table);
+    *head = pmn::AdamwTable{pmn::ADAMW_MAGIC, state_bits, count, 0, total, 0};
+    pmn::AdamwEntry* e = reinterpret_cast<pmn::AdamwEntry*>(head + 1);
+    pmn::AdamwChunk* c = reinterpret_cast<pmn::AdamwChunk*>(e + count);
+    for (int i = 0; i < count; i++) {
+        const pmn_adamw_tensor& t = tensors[i];
+        e[i] = pmn::AdamwEntry{t.param, t.grad, t.copy, t.m, t.v, t.m_e8m0, t.v_e8m0, t.n, t.weight_decay,
+                               t.grad_dtype == PMN_DTYPE_F32};
+        for (int64_t k = 0; k < adamw_chunks_of(t.n); k++) *c++ = pmn::AdamwChunk{i, (int32_t)k};
+    }
+    *chunks = total;
+    return PMN_OK;
+}
+
+int adamw_step(const void* table, int64_t chunks, int state_bits, double lr, double beta1, double beta2, double eps,
+               int64_t step, const float* lr_dev, const int64_t* step_dev, const float* grad_scale_dev,
+               uint64_t seed, uint32_t rng_stream, pmn_stream_t stream)
+{
+    if ((state_bits != 8 && state_bits != 32) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !(eps >= 0.0) || !std::isfinite(lr) || step < 1)
+        return PMN_EINVAL;
+    if (chunks < 0 || chunks >= ((int64_t)1 << 31)) return PMN_ESHAPE;
+    if (chunks == 0) return PMN_OK;
+    if (!table) return PMN_EINVAL;
+    if (!aligned(table, 8) || !aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(grad_scale_dev, 4))
+        return PMN_EALIGN;
+    const pmn::AdamwScalars a{(float)lr, (float)beta1, (float)beta2, (float)(1.0 - beta1), (float)(1.0 - beta2),
+                              (float)eps, std::log(beta1), std::log(beta2), step, lr_dev, step_dev, grad_scale_dev,
+                              seed, rng_stream};
+    return status(pmn::launch_adamw(table, chunks, state_bits, a, hs(stream)));
 }
 
 }  // extern "C"

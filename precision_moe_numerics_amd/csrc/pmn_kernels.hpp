@@ -140,4 +140,58 @@ int grouped_gemm_bwd_run(const void* dy, const uint8_t* a_codes, const uint8_t* 
                          size_t* workspace_needed, bool swiglu = false, const float* swi_da = nullptr,
                          const void* swi_h13 = nullptr);
 
+// ---- operators around the routed experts ----------------------------------------------------
+
+// z = x + res (res null: z = x, z_out unused), y = z rstd gamma; y / codes + e8m0 / rstd nullable
+hipError_t launch_rmsnorm_fwd(const uint16_t* x, const void* res, bool res_f32, const float* gamma, float eps,
+                              int64_t rows, int64_t C, void* z, uint16_t* y, uint8_t* codes, uint8_t* e8m0,
+                              float* rstd, hipStream_t stream);
+size_t rmsnorm_bwd_ws_bytes(int64_t rows, int64_t C);
+// dz in z's type (+ dres, nullable), dgamma fp32; part: rmsnorm_bwd_ws_bytes of partial sums
+hipError_t launch_rmsnorm_bwd(const void* dy, bool dy_f32, const void* z, bool z_f32, const float* gamma,
+                              const float* rstd, const void* dres, int64_t rows, int64_t C, void* dz, float* dgamma,
+                              float* part, hipStream_t stream);
+
+hipError_t launch_ffn_fwd(const uint16_t* x, const uint16_t* w13, const uint16_t* w2, const uint16_t* add, int64_t M,
+                          int64_t H, int64_t F, uint16_t* a, uint16_t* h13, uint16_t* y, hipStream_t stream);
+// dx null: no dgrad; dw13 null: no wgrad. M == 0 writes zero weight gradients.
+hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
+                          const uint16_t* h13, int64_t M, int64_t H, int64_t F, uint16_t* dh13, uint16_t* a,
+                          uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream);
+
+// The AdamW table on the device: this header, `count` entries, `chunks` chunk records.
+constexpr uint32_t ADAMW_MAGIC = 0x57414450u;
+struct AdamwTable {
+    uint32_t magic;
+    int32_t bits, count, pad;
+    int64_t chunks, pad2;
+};
+struct AdamwEntry {
+    void* param;
+    const void* grad;
+    void* copy;
+    void* m;
+    void* v;
+    uint8_t* m_e8m0;
+    uint8_t* v_e8m0;
+    int64_t n;
+    float weight_decay;
+    int32_t grad_f32;
+};
+struct AdamwChunk {
+    int32_t tensor, index;   // values index * adamw_chunk() .. of the tensor
+};
+struct AdamwScalars {
+    float lr, beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
+    double ln_beta1, ln_beta2;
+    int64_t step;
+    const float* lr_dev;             // nullable: read instead of lr, step
+    const int64_t* step_dev;
+    const float* grad_scale_dev;     // nullable: 1
+    uint64_t seed;
+    uint32_t rng_stream;
+};
+int64_t adamw_chunk();
+hipError_t launch_adamw(const void* table, int64_t chunks, int bits, const AdamwScalars& a, hipStream_t stream);
+
 }  // namespace pmn
