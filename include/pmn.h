@@ -498,7 +498,7 @@ int rmsnorm_residual_bwd(const void* dy, int dy_dtype, const void* z, int z_dtyp
  * x bf16 [M x H]; w13 bf16 [2F x H] (rows 0 .. F-1 w1, F .. 2F-1 w3); w2 bf16 [H x F]; add: NULL, or
  * bf16 [M x H] (the routed experts' sum; it may be y itself); h13_out: NULL, or bf16 [M x 2F], h1 | h3
  * for the backward; y bf16 [M x H]. a is rounded to bf16 for the second product.
- * H % 8 == 0, F % 8 == 0, M >= 0 (PMN_ESHAPE); pointers 16-byte aligned (PMN_EALIGN). Workspace
+ * H % 8 == 0, F % 8 == 0, H and F <= 2^20, 0 <= M <= 2^22 (PMN_ESHAPE); pointers 16-byte aligned (PMN_EALIGN). Workspace
  * (16-byte aligned, at least swiglu_ffn_fwd_workspace_size() bytes, PMN_EWORKSPACE).
  */
 size_t swiglu_ffn_fwd_workspace_size(int64_t M, int64_t H, int64_t F);
@@ -529,8 +529,9 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
  * state_bits 32: m, v fp32 [n]. state_bits 8: m and v uint8 [n] with m_e8m0, v_e8m0 uint8
  * [ceil(n / 32)], MXFP8 over runs of 32 values of m and of sqrt(v) (zero bytes are zero moments),
  * rounded stochastically as the requant rounds: value i of tensor j of the list draws index i under
- * seed + step and stream rng_stream + 2 j (m) or rng_stream + 2 j + 1 (v); a root above zero gets at
- * least the smallest code. The update uses the moments before their rounding.
+ * seed + step and stream rng_stream + 2 j (m) or rng_stream + 2 j + 1 (v), its place on the grid taken
+ * from value * powf(2, -e) in fp32 (as torch.ldexp scales); a root above zero gets at least the
+ * smallest code. The update uses the moments before their rounding.
  */
 typedef struct {
     float* param;         /* [n] */

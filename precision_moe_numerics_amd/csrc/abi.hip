@@ -514,16 +514,16 @@ int rmsnorm_residual_bwd(const void* dy, int dy_dtype, const void* z, int z_dtyp
                                           rows, cols, dz, dgamma, static_cast<float*>(workspace), hs(stream)));
 }
 
-// sizes whose matrices stay below 2^46 values and whose tile grids fit a launch
+// a tile's rows stay within 32-bit offsets of its first, and tile grids fit a launch
 static bool bad_ffn_shape(int64_t M, int64_t H, int64_t F)
 {
-    const int64_t most = (int64_t)1 << 22;
-    return M < 0 || M > most || H <= 0 || H > most || H % 8 != 0 || F <= 0 || F > most || F % 8 != 0;
+    const int64_t most = (int64_t)1 << 20;
+    return M < 0 || M > 4 * most || H <= 0 || H > most || H % 8 != 0 || F <= 0 || F > most || F % 8 != 0;
 }
 
 size_t swiglu_ffn_fwd_workspace_size(int64_t M, int64_t H, int64_t F)
 {
-    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 2);
+    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 2) + pmn::ffn_part_bytes(M, H, F, false);
 }
 
 int swiglu_ffn_fwd(const void* x, const void* w13, const void* w2, const void* add, int64_t M, int64_t H, int64_t F,
@@ -538,13 +538,15 @@ int swiglu_ffn_fwd(const void* x, const void* w13, const void* w2, const void* a
         return PMN_EALIGN;
     return status(pmn::launch_ffn_fwd(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w13),
                                       static_cast<const uint16_t*>(w2), static_cast<const uint16_t*>(add), M, H, F,
-                                      static_cast<uint16_t*>(workspace), static_cast<uint16_t*>(h13_out),
-                                      static_cast<uint16_t*>(y), hs(stream)));
+                                      static_cast<uint16_t*>(workspace),
+                                      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256((size_t)(M * F) * 2)),
+                                      static_cast<uint16_t*>(h13_out), static_cast<uint16_t*>(y), hs(stream)));
 }
 
 size_t swiglu_ffn_bwd_workspace_size(int64_t M, int64_t H, int64_t F)
 {
-    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 4) + round256((size_t)(M * F) * 2);
+    return bad_ffn_shape(M, H, F) ? 0 : round256((size_t)(M * F) * 4) + round256((size_t)(M * F) * 2) +
+                                        pmn::ffn_part_bytes(M, H, F, true);
 }
 
 int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w2, const void* h13, int64_t M,
@@ -567,7 +569,8 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
     return status(pmn::launch_ffn_bwd(
         static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w13),
         static_cast<const uint16_t*>(w2), static_cast<const uint16_t*>(h13), M, H, F, reinterpret_cast<uint16_t*>(ws),
-        reinterpret_cast<uint16_t*>(ws + round256((size_t)(M * F) * 4)), dgrad ? static_cast<uint16_t*>(dx) : nullptr,
+        reinterpret_cast<uint16_t*>(ws + round256((size_t)(M * F) * 4)),
+        reinterpret_cast<float*>(ws + round256((size_t)(M * F) * 4) + round256((size_t)(M * F) * 2)), dgrad ? static_cast<uint16_t*>(dx) : nullptr,
         wgrad ? dw13 : nullptr, dw2, dw_dtype == PMN_DTYPE_F32, hs(stream)));
 }
 

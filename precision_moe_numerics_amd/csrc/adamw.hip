@@ -127,9 +127,12 @@ PMN_DEV void store_codes(uint8_t* p, uint8_t* e8m0, int n, const float (&v)[8], 
     const int e = e8m0_exponent<E8M0_E4M3>(quad_max4(amax));
     uint32_t rw[4], w[2] = {0u, 0u};
     rand16x8(seed, stream, blk, rw);
+    // 2^-e as torch.ldexp forms it, by powf, which for some e is one ulp low (never high, so a block's
+    // largest value stays within 448): states packed by torch operations have the same codes
+    const float inv = powf(2.0f, (float)-e);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        uint32_t c = e4m3_sr(__builtin_ldexpf(v[j], -e), sr_operand(rw[j >> 1], j & 1));
+        uint32_t c = e4m3_sr(v[j] * inv, sr_operand(rw[j >> 1], j & 1));
         if (POSITIVE && v[j] > 0.0f && c == 0u) c = 1u;
         w[j >> 2] |= c << (8 * (j & 3));
     }
@@ -189,8 +192,10 @@ __global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __rest
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         const float gj = g[j] * gs;
-        m[j] = __builtin_fmaf(a.beta1, m[j], a.one_minus_beta1 * gj);
-        v[j] = __builtin_fmaf(a.beta2, v[j], a.one_minus_beta2 * gj * gj);
+        // each product and sum rounded by itself (no fma): the moments' bits, and with them the
+        // choices of the stochastic rounding, are those of the formula as written
+        m[j] = a.beta1 * m[j] + a.one_minus_beta1 * gj;
+        v[j] = a.beta2 * v[j] + a.one_minus_beta2 * gj * gj;
         root[j] = sqrtf(v[j]);
         const float d = __builtin_fmaf(root[j], rsbc2, a.eps);
         p[j] = __builtin_fmaf(-lrm, m[j] / d, p[j] * decay);

@@ -6,22 +6,41 @@
 // x, y, dy [M x H], w13 [2F x H] (w1 over w3), w2 [H x F], h13 [M x 2F], all row-major.
 //
 // Every product is out[c, r] = sum_k R(r, k) C(c, k) on v_mfma_f32_32x32x16_bf16 with fp32
-// accumulators: "R" supplies the matrix rows (output features, so that a lane holds 4 consecutive
-// ones of one output row), "C" the columns. An operand is either k-contiguous (rows of the matrix
-// are rows of the product) or row-contiguous (the matrix is stored transposed: the weights in dgrad,
-// both operands in wgrad).
+// accumulators. "R" supplies the accumulator's rows (columns of the output: an output row's values
+// stand 4 in a lane), "C" its columns. An operand is either k-contiguous (KC: its stored rows are rows
+// of the product) or row-contiguous (RC: stored transposed, one stored row per k: the weights in
+// dgrad, both operands in wgrad).
+//
+// Operands stream through a ring of LDS stages of 32 k, filled by buffer_load ... lds (global -> LDS
+// without registers), 1 KB pieces dealt evenly to the wavefronts, so "stage s has landed" is the
+// per-wavefront condition vmcnt <= pieces issued after it, followed by a barrier. A wavefront reads the
+// fragments of stage v + 1 while the MFMAs of stage v run from registers. Bounds are the buffer
+// descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
+// the same code.
+//   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
+//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured).
+//   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
+//     of 16 the column i of 4 k; the 32-byte pairs of chunks of row k are permuted by
+//     ((k / 8) % 2) | 2 (k % 4), so that the 4 k of 16 lanes lie in different banks (174 B/clk/CU
+//     measured; 64 without).
+//
+// The accumulators leave through LDS, 32 output rows of a wavefront column at a time, so that a
+// thread finishes 8 consecutive values of an output row with 16-byte accesses. Where the tiles of a
+// product are fewer than the compute units the contraction is split: the parts write fp32 sums and a
+// second kernel adds them in order and finishes the rows, so results do not depend on the launch.
+#include <type_traits>
+
 #include "pmn_dev.hpp"
 #include "pmn_kernels.hpp"
 
 namespace pmn {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-namespace ffn {
-constexpr int BT = 128, BK = 32, THREADS = 256, PITCH = BK + 8;
-}
-
-enum { FFN_SWIGLU = 0, FFN_ADD = 1, FFN_SWIGLU_BWD = 2, FFN_BF16 = 3, FFN_F32 = 4 };
+enum { FFN_SWIGLU = 0, FFN_ADD = 1, FFN_SWIGLU_BWD = 2, FFN_BF16 = 3, FFN_F32 = 4, FFN_PART = 5 };
 
 struct FfnArgs {
     const uint16_t* r;      // R operand, ldr elements between its stored rows
@@ -32,171 +51,455 @@ struct FfnArgs {
     const uint16_t* aux;    // ADD: add (or null); SWIGLU_BWD: h13
     uint16_t* out2;         // SWIGLU: h13 (or null); SWIGLU_BWD: a
     int64_t F;
+    float* part;            // PART: [splits x Nc x Nr]
+    int splits;
+    int64_t rtiles, ctiles;
+    int SM, SN;
 };
 
-// Stage a 128 x 32 operand tile as lds[row][k]. KC: 16-byte pieces of 8 k; else 8 rows at one k.
-template <bool KC, typename RowOf>
-PMN_DEV void stage_tile(const uint16_t* src, int64_t ld, int64_t nrows, int64_t k0, int64_t K, RowOf row_of,
-                        uint16_t (*lds)[ffn::PITCH])
+// 8 consecutive outputs n .. n+7 of output row c from their fp32 sums (SWIGLU: v = h1, v2 = h3 of
+// features n .. n+7). aux is read and out written only here, so out may be aux itself.
+template <int EPI>
+PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], float (&v2)[8])
 {
-    using namespace ffn;
+    auto put = [](uint16_t* dst, const float (&o)[8]) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]),
+                                                    bf16x2_bits(o[4], o[5]), bf16x2_bits(o[6], o[7]));
+    };
+    auto get = [](const uint16_t* src, float (&o)[8]) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int q = 0; q < BT * BK / 8 / THREADS; q++) {
-        const int p = q * THREADS + threadIdx.x;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (KC) {
-            const int row = p >> 2, kc = (p & 3) * 8;
-            const int64_t r = row_of(row);
-            if (r >= 0 && k0 + kc < K) w = *reinterpret_cast<const uint4*>(src + r * ld + k0 + kc);
-            *reinterpret_cast<uint4*>(&lds[row][kc]) = w;
-        } else {
-            const int k = p >> 4, rc = (p & 15) * 8;
-            const int64_t r = row_of(rc);
-            if (r >= 0 && k0 + k < K) w = *reinterpret_cast<const uint4*>(src + (k0 + k) * ld + r);
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 8; j++) lds[rc + j][k] = (uint16_t)(j & 1 ? a[j >> 1] >> 16 : a[j >> 1]);
+        for (int q = 0; q < 4; q++) {
+            o[2 * q] = bf16_lo(a[q]);
+            o[2 * q + 1] = bf16_hi(a[q]);
         }
+    };
+    if (EPI == FFN_SWIGLU) {
+        float a[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) a[u] = silu(v[u]) * v2[u];
+        put(static_cast<uint16_t*>(p.out) + c * p.F + n, a);
+        if (p.out2) {
+            put(p.out2 + c * 2 * p.F + n, v);
+            put(p.out2 + c * 2 * p.F + p.F + n, v2);
+        }
+    } else if (EPI == FFN_SWIGLU_BWD) {
+        float h1[8], h3[8], a[8];
+        get(p.aux + c * 2 * p.F + n, h1);
+        get(p.aux + c * 2 * p.F + p.F + n, h3);
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            // silu'(h) = s (1 + h (1 - s)); the values are rounded to bf16, far coarser than the
+            // hardware exp2 and reciprocal
+            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-h1[u] * 1.44269504088896341f));
+            a[u] = h1[u] * s * h3[u];
+            v2[u] = v[u] * h1[u] * s;
+            v[u] = v[u] * h3[u] * (s * (1.0f + h1[u] * (1.0f - s)));
+        }
+        put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + n, v);
+        put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + p.F + n, v2);
+        put(p.out2 + c * p.F + n, a);
+    } else if (EPI == FFN_F32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + c * p.Nr + n);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        if (EPI == FFN_ADD && p.aux) {
+            float b[8];
+            get(p.aux + c * p.Nr + n, b);
+#pragma unroll
+            for (int u = 0; u < 8; u++) v[u] += b[u];
+        }
+        put(static_cast<uint16_t*>(p.out) + c * p.Nr + n, v);
     }
 }
 
-template <bool RKC, bool CKC, int EPI>
-__global__ __launch_bounds__(ffn::THREADS) void k_ffn_gemm(FfnArgs p)
+// buffer descriptor of `bytes` bytes (at most 2^31 - 1) from p: loads past them return zero
+PMN_DEV i32x4 buffer_of(const void* p, int64_t bytes)
 {
-    using namespace ffn;
-    __shared__ __attribute__((aligned(16))) uint16_t lr[BT][PITCH], lc[BT][PITCH];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wr = wave >> 1, wc = wave & 1, l32 = lane & 31, hh = lane >> 5;
-    const int64_t c0 = (int64_t)blockIdx.y * BT;
-    // SWIGLU: a tile holds 64 features, w1 and w3 rows of the same feature in blocks 0 and 1 of a wavefront
-    const int64_t r0 = (int64_t)blockIdx.x * (EPI == FFN_SWIGLU ? BT / 2 : BT);
-    auto row_r = [&](int t) -> int64_t {
-        if (EPI == FFN_SWIGLU) {
-            const int64_t f = r0 + (t >> 6) * 32 + (t & 31);
-            return f < p.F ? ((t >> 5) & 1) * p.F + f : -1;
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const int n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes);
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                 __builtin_amdgcn_readfirstlane(n), 0x00020000};
+}
+
+// 16 bytes per lane from buffer offset voff (past the buffer: zeros) to LDS lds + 16 lane. The
+// s_nop is the wait state that an LDS load needs after a write of m0.
+PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+constexpr uint32_t FFN_OUTSIDE = 0x80000000u;   // a buffer offset past every descriptor
+
+// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages
+template <int WR_, int WC_, int RB_, int CB_, int NST_>
+struct FfnTile {
+    static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
+    static constexpr int BR = WR * RB * 32, BC = WC * CB * 32;
+    static constexpr int THREADS = WR * WC * 64;
+    static constexpr int RBYTES = BR * 64, STAGE = (BR + BC) * 64;
+    static constexpr int PIECES = STAGE / 1024, PPW = PIECES / (WR * WC), RPIECES = RBYTES / 1024;
+    static constexpr int OPITCH = BR + 4;                       // floats per staged output row
+    static constexpr int OROWS = WC * 32;                       // output rows staged at a time
+    static constexpr int RING = NST * STAGE, OUTB = OROWS * OPITCH * 4;
+    static constexpr int LDS = RING > OUTB ? RING : OUTB;
+    static_assert(PIECES % (WR * WC) == 0, "every wavefront loads the same number of pieces");
+    static_assert((NST - 2) * PPW <= 63, "vmcnt");
+};
+
+template <typename T, bool RKC, bool CKC, int EPI>
+__global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(FfnArgs p)
+{
+    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, PPW = T::PPW;
+    constexpr bool SWI = EPI == FFN_SWIGLU;
+    static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+    if (RB == 4) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave / T::WC, wc = wave % T::WC, l32 = lane & 31, hh = lane >> 5;
+
+    TileXY tile;
+    int64_t L = blockIdx.x;
+    int split = 0;
+    if (EPI == FFN_PART) {
+        split = (int)(L % p.splits);
+        L /= p.splits;
+        tile.row = L % p.rtiles;
+        tile.col = L / p.rtiles;
+    } else if (!xcd_tile(L, p.rtiles, p.ctiles, p.SM, p.SN, tile)) {
+        return;
+    }
+    const int64_t r0 = tile.row * (SWI ? BR / 2 : BR), c0 = tile.col * BC;
+    const int64_t KT = (p.K + 31) >> 5;
+    const int64_t s0 = EPI == FFN_PART ? KT * split / p.splits : 0;
+    const int64_t s1 = EPI == FFN_PART ? KT * (split + 1) / p.splits : KT;
+    const int nst = (int)(s1 - s0);
+
+    // this wavefront's pieces: byte offset of the lane's 16 bytes from the stage's first k, and for a
+    // k-contiguous operand the lane's first k of the stage
+    uint32_t voff[PPW];
+    int kch[PPW];
+#pragma unroll
+    for (int i = 0; i < PPW; i++) {
+        const int pc = wave * PPW + i;
+        const bool isr = pc < T::RPIECES;
+        const int q = isr ? pc : pc - T::RPIECES;
+        const int64_t ld = isr ? p.ldr : p.ldc;
+        if (isr ? RKC : CKC) {
+            const int t = q * 16 + (lane >> 2);                       // tile row
+            const int ch = (lane & 3) ^ ((t >> 2) & 3);
+            int row = t;                                              // from the tile's first
+            bool ok;
+            if (SWI && isr) {
+                // features of w1 (blocks 0 .. RB / 2 - 1 of a wavefront) or w3 (the others)
+                row = (t / (32 * RB)) * (16 * RB) + ((t >> 5) % (RB / 2)) * 32 + (t & 31);
+                ok = r0 + row < p.F;
+            } else {
+                ok = (isr ? r0 : c0) + t < (isr ? p.Nr : p.Nc);
+            }
+            voff[i] = ok ? (uint32_t)(row * ld * 2 + ch * 16) : FFN_OUTSIDE;
+            kch[i] = ch * 8;
+        } else {
+            const int W = isr ? BR * 2 : BC * 2;                      // bytes of a stored row in the tile
+            const int k = (q * 1024 + lane * 16) / W, ch = (q * 1024 + lane * 16) % W / 16;
+            const int sw = ((k >> 3) & 1) | ((k & 3) << 1);
+            const int col = ((((ch >> 1) ^ sw) << 1) | (ch & 1)) * 8;
+            const bool ok = (isr ? r0 : c0) + col < (isr ? p.Nr : p.Nc);
+            voff[i] = ok ? (uint32_t)(k * ld * 2 + col * 2) : FFN_OUTSIDE;
+            kch[i] = 0;
         }
-        return r0 + t < p.Nr ? r0 + t : -1;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
+    const uint32_t ldst = lds0 + wave * PPW * 1024;
+    // descriptor of an operand at stage s of this part (nothing past its last stage)
+    auto rsrc_at = [&](bool isr, int s) {
+        const uint16_t* base = isr ? p.r : p.c;
+        const int64_t ld = isr ? p.ldr : p.ldc, k0 = (s0 + s) * 32;
+        const bool kc = isr ? RKC : CKC;
+        if (kc) return buffer_of(base + (isr ? r0 : c0) * ld + k0, s < nst ? (int64_t)0x7FFFFFFF : 0);
+        return buffer_of(base + k0 * ld + (isr ? r0 : c0), s < nst ? ((p.K - k0) * ld - (isr ? r0 : c0)) * 2 : 0);
     };
-    auto row_c = [&](int t) -> int64_t { return c0 + t < p.Nc ? c0 + t : -1; };
-    f32x16 acc[2][2];
+    struct Stage {
+        i32x4 rr, rc, r3;
+        int left;
+        uint32_t dst;
+    };
+    auto stage_at = [&](int s) {
+        Stage g;
+        g.rr = rsrc_at(true, s);
+        g.rc = rsrc_at(false, s);
+        if (SWI) g.r3 = buffer_of(p.r + (p.F + r0) * p.ldr + (s0 + s) * 32, s < nst ? (int64_t)0x7FFFFFFF : 0);
+        const int64_t left = p.K - (s0 + s) * 32;
+        g.left = left > 32 ? 32 : (int)left;
+        g.dst = ldst + (uint32_t)(s % NST) * T::STAGE;
+        return g;
+    };
+    auto issue_piece = [&](const Stage& g, int i) {
+        const int pc = wave * PPW + i;
+        const bool isr = pc < T::RPIECES;
+        const bool w3 = SWI && isr && (pc >> 1) % RB >= RB / 2;
+        // chunks past K of a k-contiguous operand
+        const uint32_t v = (isr ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i];
+        dma16_buffer(w3 ? g.r3 : (isr ? g.rr : g.rc), v, g.dst + i * 1024);
+    };
+
+    struct Frags {
+        bf16x8 r[RB][2], c[CB][2];
+    };
+    // lane constants of the fragment reads
+    const int swz = (l32 >> 2) & 3;
+    const int g16 = lane >> 4, i16 = lane & 15, swt = (g16 >> 1) | ((i16 >> 2) << 1);
+    auto read_frag = [&](const uint8_t* base, auto kc, int width, int blk, int ks) -> bf16x8 {
+        if constexpr (decltype(kc)::value) {
+            return *reinterpret_cast<const bf16x8*>(base + (blk * 32 + l32) * 64 + (((2 * ks + hh) ^ swz) << 4));
+        } else {
+            // columns 32 blk + 16 (g16 % 2) .., k = 16 ks + 8 (g16 / 2) + i16 / 4 and 4 further
+            const int pair = (2 * blk + (g16 & 1)) ^ swt;
+            const uint8_t* a = base + (16 * ks + 8 * (g16 >> 1) + (i16 >> 2)) * width + pair * 32 + (i16 & 3) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(a + 4 * width));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    };
+    constexpr int NREAD = 2 * (RB + CB);
+    auto read_one = [&](const uint8_t* base, int n, Frags& f) {
+        const int ks = n / (RB + CB), b = n % (RB + CB);
+        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks);
+        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks);
+    };
+
+    f32x16 acc[RB][CB];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < RB; i++)
 #pragma unroll
-        for (int j = 0; j < 2; j++)
+        for (int j = 0; j < CB; j++)
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
-    for (int64_t k0 = 0; k0 < p.K; k0 += BK) {
-        __syncthreads();
-        stage_tile<RKC>(p.r, p.ldr, p.Nr, k0, p.K, row_r, lr);
-        stage_tile<CKC>(p.c, p.ldc, p.Nc, k0, p.K, row_c, lc);
-        __syncthreads();
+
+    // One step: stage v + 1 has landed and every wavefront is done reading stage v, whose slot is
+    // refilled with stage v + NST. The step's loads and fragment reads are spread over its MFMAs.
+    constexpr int NM = 2 * RB * CB, NA = PPW + NREAD;
+    auto step = [&](int v, const Frags& cur, Frags& nxt) {
+        wait_loads_and_barrier<(NST - 2) * PPW>();
+        const Stage g = stage_at(v + NST);
+        const uint8_t* rbase = lds + ((v + 1) % NST) * T::STAGE;
 #pragma unroll
-        for (int ks = 0; ks < BK; ks += 16) {
-            bf16x8 a[2], b[2];
+        for (int q = 0; q < NM; q++) {
+            const int ks = q / (RB * CB), i = (q / CB) % RB, j = q % CB;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cur.r[i][ks], cur.c[j][ks], acc[i][j], 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                a[i] = *reinterpret_cast<const bf16x8*>(&lr[wr * 64 + i * 32 + l32][ks + 8 * hh]);
-                b[i] = *reinterpret_cast<const bf16x8*>(&lc[wc * 64 + i * 32 + l32][ks + 8 * hh]);
+            for (int n = q * NA / NM; n < (q + 1) * NA / NM; n++) {
+                if (n < PPW) issue_piece(g, n);
+                else read_one(rbase, n - PPW, nxt);
             }
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    {
+#pragma unroll
+        for (int s = 0; s < NST; s++) {
+            const Stage g = stage_at(s);
+#pragma unroll
+            for (int i = 0; i < PPW; i++) issue_piece(g, i);
+        }
+        Frags f0, f1;
+        wait_loads_and_barrier<(NST - 1) * PPW>();
+#pragma unroll
+        for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
+        for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
+            step(v, f0, f1);
+            step(v + 1, f1, f0);
+        }
+        wait_loads_and_barrier<0>();
     }
+
+    // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]
+    float* const ot = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-        const int64_t c = c0 + wc * 64 + j * 32 + l32;
-        if (c >= p.Nc) continue;
+    for (int j = 0; j < CB; j++) {
+        if (j > 0) __syncthreads();
+        float* const row = ot + (wc * 32 + l32) * T::OPITCH;
 #pragma unroll
-        for (int i = 0; i < (EPI == FFN_SWIGLU ? 1 : 2); i++) {
+        for (int i = 0; i < RB; i++) {
+            // SWIGLU: h1 in the first half of the row, h3 in the second
+            const int n = SWI ? (i / (RB / 2)) * (BR / 2) + wr * 16 * RB + (i % (RB / 2)) * 32 : (wr * RB + i) * 32;
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int64_t n = r0 + (EPI == FFN_SWIGLU ? wr * 32 : wr * 64 + i * 32) + q * 8 + hh * 4;
-                if (n >= (EPI == FFN_SWIGLU ? p.F : p.Nr)) continue;   // sizes are multiples of 8
-                float o[4];
+            for (int q = 0; q < 4; q++)
+                *reinterpret_cast<float4*>(row + n + q * 8 + hh * 4) =
+                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+        constexpr int NW = (SWI ? BR / 2 : BR) / 8;                 // 8-value pieces of a staged row
+        for (int k = tid; k < T::OROWS * NW; k += T::THREADS) {
+            const int rr = k / NW, n = (k % NW) * 8;
+            const int64_t c = c0 + (rr >> 5) * (32 * CB) + j * 32 + (rr & 31);
+            if (c >= p.Nc || r0 + n >= (SWI ? p.F : p.Nr)) continue;
+            const float* src = ot + rr * T::OPITCH + n;
+            float v[8], v2[8];
 #pragma unroll
-                for (int u = 0; u < 4; u++) o[u] = acc[i][j][4 * q + u];
-                auto put = [&](uint16_t* dst, const float (&v)[4]) {
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
-                };
-                if (EPI == FFN_SWIGLU) {
-                    float h3[4], a[4];
-#pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        h3[u] = acc[1][j][4 * q + u];
-                        a[u] = silu(o[u]) * h3[u];
-                    }
-                    put(static_cast<uint16_t*>(p.out) + c * p.F + n, a);
-                    if (p.out2) {
-                        put(p.out2 + c * 2 * p.F + n, o);
-                        put(p.out2 + c * 2 * p.F + p.F + n, h3);
-                    }
-                } else if (EPI == FFN_SWIGLU_BWD) {
-                    const uint2 w1 = *reinterpret_cast<const uint2*>(p.aux + c * 2 * p.F + n);
-                    const uint2 w3 = *reinterpret_cast<const uint2*>(p.aux + c * 2 * p.F + p.F + n);
-                    const float h1[4] = {bf16_lo(w1.x), bf16_hi(w1.x), bf16_lo(w1.y), bf16_hi(w1.y)};
-                    const float h3[4] = {bf16_lo(w3.x), bf16_hi(w3.x), bf16_lo(w3.y), bf16_hi(w3.y)};
-                    float d1[4], d3[4], a[4];
-#pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-h1[u] * 1.44269504088896341f));
-                        d1[u] = o[u] * h3[u] * (s * (1.0f + h1[u] * (1.0f - s)));
-                        d3[u] = o[u] * h1[u] * s;
-                        a[u] = h1[u] * s * h3[u];
-                    }
-                    put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + n, d1);
-                    put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + p.F + n, d3);
-                    put(p.out2 + c * p.F + n, a);
-                } else if (EPI == FFN_F32) {
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + c * p.Nr + n) =
-                        make_float4(o[0], o[1], o[2], o[3]);
-                } else {
-                    if (EPI == FFN_ADD && p.aux) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(p.aux + c * p.Nr + n);
-                        o[0] += bf16_lo(w.x); o[1] += bf16_hi(w.x); o[2] += bf16_lo(w.y); o[3] += bf16_hi(w.y);
-                    }
-                    put(static_cast<uint16_t*>(p.out) + c * p.Nr + n, o);
+            for (int u = 0; u < 8; u += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(src + u);
+                v[u] = a.x; v[u + 1] = a.y; v[u + 2] = a.z; v[u + 3] = a.w;
+                if (SWI) {
+                    const float4 b = *reinterpret_cast<const float4*>(src + BR / 2 + u);
+                    v2[u] = b.x; v2[u + 1] = b.y; v2[u + 2] = b.z; v2[u + 3] = b.w;
                 }
+            }
+            if constexpr (EPI == FFN_PART) {
+                float4* dst = reinterpret_cast<float4*>(p.part + ((int64_t)split * p.Nc + c) * p.Nr + r0 + n);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                ffn_finish8<EPI>(p, c, r0 + n, v, v2);
             }
         }
     }
 }
 
-template <bool RKC, bool CKC, int EPI>
-static void ffn_gemm(const FfnArgs& p, hipStream_t stream)
+// Finish a split product: the parts of 8 consecutive outputs added in order. One thread each.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
 {
-    const int64_t rt = ffn::BT / (EPI == FFN_SWIGLU ? 2 : 1), n = EPI == FFN_SWIGLU ? p.F : p.Nr;
-    hipLaunchKernelGGL((k_ffn_gemm<RKC, CKC, EPI>), dim3((unsigned)((n + rt - 1) / rt), (unsigned)((p.Nc + ffn::BT - 1) / ffn::BT)),
-                       dim3(ffn::THREADS), 0, stream, p);
+    const int64_t per = (EPI == FFN_SWIGLU ? p.F : p.Nr) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.Nc * per) return;
+    const int64_t c = i / per, n = (i - c * per) * 8;
+    float v[8], v2[8];
+    auto sum = [&](int64_t col, float (&o)[8]) {
+#pragma unroll
+        for (int u = 0; u < 8; u++) o[u] = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < p.splits; s++) {
+            const float4* src = reinterpret_cast<const float4*>(p.part + ((int64_t)s * p.Nc + c) * p.Nr + col);
+            const float4 a = src[0], b = src[1];
+            o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+            o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+        }
+    };
+    sum(n, v);
+    if (EPI == FFN_SWIGLU) sum(p.F + n, v2);
+    ffn_finish8<EPI>(p, c, n, v, v2);
+}
+
+typedef FfnTile<2, 2, 4, 4, 4> FfnLarge;    // 256 x 256, one workgroup per CU
+typedef FfnTile<2, 2, 2, 2, 4> FfnMid;      // 128 x 128
+typedef FfnTile<4, 1, 1, 2, 6> FfnFew;      // 128 x 64: few output rows, the R operand streams
+
+constexpr int FFN_CUS = 256;   // the split's target; fixed, so that results depend on the sizes alone
+
+struct FfnPlan {
+    int tile;      // 0 large, 1 mid, 2 few
+    int splits;    // 0: no split
+};
+
+// Tile and split of a product of Nc x Nr outputs over K.
+static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
+{
+    if (Nc == 0) return {1, 0};
+    auto tiles = [&](int64_t br, int64_t bc) { return ((Nr + br - 1) / br) * ((Nc + bc - 1) / bc); };
+    const int64_t stages = (K + 31) / 32;
+    auto split_for = [&](int64_t t, int64_t want, int64_t least) {
+        int64_t s = (want + t - 1) / t;
+        const int64_t most = stages / least;
+        s = s > most ? most : s;
+        return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    };
+    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), 2 * FFN_CUS, 8)};
+    if (tiles(256, 256) >= 160) return {0, 0};
+    const int64_t t = tiles(128, 128);
+    if (t >= FFN_CUS || stages < 32) return {1, 0};
+    const int s = split_for(t, 2 * FFN_CUS, 16);
+    return {1, s > 1 ? s : 0};
+}
+
+static int64_t ffn_part_floats(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
+{
+    return (int64_t)ffn_plan(Nc, Nr, K, ckc).splits * Nc * Nr;
+}
+
+template <typename T, bool RKC, bool CKC, int EPI>
+static void ffn_launch_tile(FfnArgs p, hipStream_t stream)
+{
+    const int64_t nr = EPI == FFN_SWIGLU ? p.F : p.Nr, br = EPI == FFN_SWIGLU ? T::BR / 2 : T::BR;
+    p.rtiles = (nr + br - 1) / br;
+    p.ctiles = (p.Nc + T::BC - 1) / T::BC;
+    int64_t grid;
+    if (EPI == FFN_PART) {
+        grid = p.rtiles * p.ctiles * p.splits;
+    } else {
+        xcd_shape(p.rtiles, p.ctiles, p.SM, p.SN);
+        grid = xcd_grid(p.rtiles, p.ctiles, p.SM, p.SN);
+    }
+    hipLaunchKernelGGL((k_ffn_gemm<T, RKC, CKC, EPI>), dim3((unsigned)grid), dim3(T::THREADS), 0, stream, p);
+}
+
+template <bool RKC, bool CKC, int EPI>
+static void ffn_gemm(FfnArgs p, float* part, hipStream_t stream)
+{
+    const FfnPlan pl = ffn_plan(p.Nc, p.Nr, p.K, CKC);
+    p.splits = pl.splits;
+    p.part = part;
+    if (pl.splits == 0) {
+        if (pl.tile == 0) ffn_launch_tile<FfnLarge, RKC, CKC, EPI>(p, stream);
+        else ffn_launch_tile<FfnMid, RKC, CKC, EPI>(p, stream);
+        return;
+    }
+    if (pl.tile == 1) ffn_launch_tile<FfnMid, RKC, CKC, FFN_PART>(p, stream);
+    else if constexpr (CKC) ffn_launch_tile<FfnFew, RKC, CKC, FFN_PART>(p, stream);
+    const int64_t n = p.Nc * ((EPI == FFN_SWIGLU ? p.F : p.Nr) / 8);
+    hipLaunchKernelGGL((k_ffn_reduce<EPI>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, p);
+}
+
+size_t ffn_part_bytes(int64_t M, int64_t H, int64_t F, bool bwd)
+{
+    int64_t n = 0;
+    auto need = [&](int64_t nc, int64_t nr, int64_t k, bool ckc) {
+        const int64_t f = ffn_part_floats(nc, nr, k, ckc);
+        n = f > n ? f : n;
+    };
+    if (!bwd) {
+        need(M, 2 * F, H, true);
+        need(M, H, F, true);
+    } else {
+        need(M, F, H, true);
+        need(M, H, 2 * F, true);
+        need(2 * F, H, M, false);
+        need(H, F, M, false);
+    }
+    return (size_t)n * sizeof(float);
 }
 
 // a [M x F] = silu(x w1^T) (x w3^T), with h13 where it is kept; y = a w2^T + add
 hipError_t launch_ffn_fwd(const uint16_t* x, const uint16_t* w13, const uint16_t* w2, const uint16_t* add, int64_t M,
-                          int64_t H, int64_t F, uint16_t* a, uint16_t* h13, uint16_t* y, hipStream_t stream)
+                          int64_t H, int64_t F, uint16_t* a, float* part, uint16_t* h13, uint16_t* y, hipStream_t stream)
 {
-    ffn_gemm<true, true, FFN_SWIGLU>(FfnArgs{w13, x, H, H, 2 * F, M, H, a, nullptr, h13, F}, stream);
-    ffn_gemm<true, true, FFN_ADD>(FfnArgs{w2, a, F, F, H, M, F, y, add, nullptr, F}, stream);
+    ffn_gemm<true, true, FFN_SWIGLU>(FfnArgs{w13, x, H, H, 2 * F, M, H, a, nullptr, h13, F}, part, stream);
+    ffn_gemm<true, true, FFN_ADD>(FfnArgs{w2, a, F, F, H, M, F, y, add, nullptr, F}, part, stream);
     return hipGetLastError();
 }
 
 // dh13 [M x 2F] and a [M x F] from dy, w2 and h13; then the gradients asked for
 hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
                           const uint16_t* h13, int64_t M, int64_t H, int64_t F, uint16_t* dh13, uint16_t* a,
-                          uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream)
+                          float* part, uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream)
 {
-    if (M > 0) ffn_gemm<false, true, FFN_SWIGLU_BWD>(FfnArgs{w2, dy, F, H, F, M, H, dh13, h13, a, F}, stream);
-    if (M > 0 && dx) ffn_gemm<false, true, FFN_BF16>(FfnArgs{w13, dh13, H, 2 * F, H, M, 2 * F, dx, nullptr, nullptr, F}, stream);
+    if (M > 0) ffn_gemm<false, true, FFN_SWIGLU_BWD>(FfnArgs{w2, dy, F, H, F, M, H, dh13, h13, a, F}, part, stream);
+    if (M > 0 && dx)
+        ffn_gemm<false, true, FFN_BF16>(FfnArgs{w13, dh13, H, 2 * F, H, M, 2 * F, dx, nullptr, nullptr, F}, part, stream);
     if (dw13) {
         const FfnArgs g13{x, dh13, H, 2 * F, H, 2 * F, M, dw13, nullptr, nullptr, F};
         const FfnArgs g2{a, dy, F, H, F, H, M, dw2, nullptr, nullptr, F};
         if (dw_f32) {
-            ffn_gemm<false, false, FFN_F32>(g13, stream);
-            ffn_gemm<false, false, FFN_F32>(g2, stream);
+            ffn_gemm<false, false, FFN_F32>(g13, part, stream);
+            ffn_gemm<false, false, FFN_F32>(g2, part, stream);
         } else {
-            ffn_gemm<false, false, FFN_BF16>(g13, stream);
-            ffn_gemm<false, false, FFN_BF16>(g2, stream);
+            ffn_gemm<false, false, FFN_BF16>(g13, part, stream);
+            ffn_gemm<false, false, FFN_BF16>(g2, part, stream);
         }
     }
     return hipGetLastError();

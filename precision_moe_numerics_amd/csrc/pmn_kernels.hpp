@@ -152,12 +152,15 @@ hipError_t launch_rmsnorm_bwd(const void* dy, bool dy_f32, const void* z, bool z
                               const float* rstd, const void* dres, int64_t rows, int64_t C, void* dz, float* dgamma,
                               float* part, hipStream_t stream);
 
+// Bytes of fp32 sums of split products (part) that a call of these sizes needs
+size_t ffn_part_bytes(int64_t M, int64_t H, int64_t F, bool bwd);
 hipError_t launch_ffn_fwd(const uint16_t* x, const uint16_t* w13, const uint16_t* w2, const uint16_t* add, int64_t M,
-                          int64_t H, int64_t F, uint16_t* a, uint16_t* h13, uint16_t* y, hipStream_t stream);
+                          int64_t H, int64_t F, uint16_t* a, float* part, uint16_t* h13, uint16_t* y,
+                          hipStream_t stream);
 // dx null: no dgrad; dw13 null: no wgrad. M == 0 writes zero weight gradients.
 hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
                           const uint16_t* h13, int64_t M, int64_t H, int64_t F, uint16_t* dh13, uint16_t* a,
-                          uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream);
+                          float* part, uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream);
 
 // The AdamW table on the device: this header, `count` entries, `chunks` chunk records.
 constexpr uint32_t ADAMW_MAGIC = 0x57414450u;
