@@ -131,9 +131,9 @@ def _need(cond: bool, what: str):
 
 
 def _tensor(t: Optional[torch.Tensor], shape, dtype, name: str):
-    _need(t is not None and t.dtype == dtype and tuple(t.shape) == tuple(shape),
-          f"{name} must be {dtype} of shape {tuple(shape)}"
-          + ("" if t is None else f", got {t.dtype} of shape {tuple(t.shape)}"))
+    if t is None or t.dtype != dtype or t.shape != shape:
+        raise PmnError(f"{name} must be {dtype} of shape {tuple(shape)}"
+                       + ("" if t is None else f", got {t.dtype} of shape {tuple(t.shape)}"))
 
 
 def _index(t: Optional[torch.Tensor], n: int, dtype, name: str):
@@ -616,14 +616,37 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
     return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
 
 
-def _one_device(**tensors):
-    """Every tensor on the current device, whose current stream the call takes."""
-    for name, t in tensors.items():
-        if t is not None:
-            if not t.is_cuda:
-                raise PmnError(f"{name} must be on the GPU")
-            if t.device.index != torch.cuda.current_device():
-                raise PmnError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _device_ptr(t: Optional[torch.Tensor], dev: int, name: str):
+    """Pointer of a contiguous tensor on device dev (None for None)."""
+    if t is None:
+        return None
+    at = t.get_device()
+    if at != dev:
+        raise PmnError(f"{name} must be on the GPU" if at < 0 else f"{name} is on cuda:{at}, the call is for cuda:{dev}")
+    if not t.is_contiguous():
+        raise PmnError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The device of t, which must be the current one: the call goes to its current stream."""
+    dev = t.get_device()
+    if dev < 0:
+        raise PmnError(f"{name} must be on the GPU")
+    if dev != torch.cuda.current_device():
+        raise PmnError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without its objects
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1, "workspace must be a 1-D uint8 tensor")
+    return workspace
 
 
 @dataclass
@@ -645,25 +668,31 @@ def rmsnorm_residual_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6
     residual itself) receives the sum. want_y: the bf16 output; want_mxfp8: the row-wise MXFP8 output;
     want_rstd: what the backward needs."""
     _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [rows, cols]")
-    R, Cc = x.shape
-    dev = x.device
+    shape = x.shape
+    R, Cc = shape
     _tensor(gamma, (Cc,), torch.float32, "gamma")
     _need(want_y or want_mxfp8, "want_y or want_mxfp8 must be set")
     _need(not want_mxfp8 or Cc % 32 == 0, "MXFP8 output needs cols to be a multiple of 32")
-    _need(residual is not None or z_out is None, "z_out needs a residual")
     rcode = DTYPE_BF16
     if residual is not None:
         rcode = _dtype_code(residual, "residual")
-        _tensor(residual, (R, Cc), residual.dtype, "residual")
-        z_out = torch.empty_like(residual) if z_out is None else z_out
-        _tensor(z_out, (R, Cc), residual.dtype, "z_out")
-    _one_device(x=x, gamma=gamma, residual=residual, z_out=z_out)
-    y = torch.empty((R, Cc), dtype=torch.bfloat16, device=dev) if want_y else None
-    codes = torch.empty((R, Cc), dtype=torch.uint8, device=dev) if want_mxfp8 else None
+        _tensor(residual, shape, residual.dtype, "residual")
+        if z_out is not None:
+            _tensor(z_out, shape, residual.dtype, "z_out")
+    else:
+        _need(z_out is None, "z_out needs a residual")
+    at = _device_of(x, "x")
+    dev = x.device
+    if residual is not None and z_out is None:
+        z_out = torch.empty_like(residual)
+    y = torch.empty_like(x) if want_y else None
+    codes = torch.empty(shape, dtype=torch.uint8, device=dev) if want_mxfp8 else None
     e8m0 = torch.empty((R, Cc // 32), dtype=torch.uint8, device=dev) if want_mxfp8 else None
-    rstd = torch.empty((R,), dtype=torch.float32, device=dev) if want_rstd else None
-    _check(_lib.rmsnorm_residual_fwd(_ptr(x), _ptr(residual), rcode, _ptr(gamma), eps, R, Cc, _ptr(z_out), _ptr(y),
-                                     _ptr(codes), _ptr(e8m0), _ptr(rstd), _stream()), "rmsnorm_residual_fwd")
+    rstd = torch.empty(R, dtype=torch.float32, device=dev) if want_rstd else None
+    _check(_lib.rmsnorm_residual_fwd(
+        _device_ptr(x, at, "x"), _device_ptr(residual, at, "residual"), rcode, _device_ptr(gamma, at, "gamma"), eps, R,
+        Cc, _device_ptr(z_out, at, "z_out"), _device_ptr(y, at, "y"), _device_ptr(codes, at, "codes"),
+        _device_ptr(e8m0, at, "e8m0"), _device_ptr(rstd, at, "rstd"), _raw_stream(at)), "rmsnorm_residual_fwd")
     return RmsNorm(y, codes, e8m0, z_out, rstd)
 
 
@@ -680,16 +709,17 @@ def rmsnorm_residual_bwd(dy: torch.Tensor, z: torch.Tensor, gamma: torch.Tensor,
     _tensor(rstd, (R,), torch.float32, "rstd")
     if dres is not None:
         _tensor(dres, (R, Cc), z.dtype, "dres")
+    if dz is not None:
+        _tensor(dz, (R, Cc), z.dtype, "dz")
+    at = _device_of(z, "z")
     dz = torch.empty_like(z) if dz is None else dz
-    _tensor(dz, (R, Cc), z.dtype, "dz")
-    if workspace is None:
-        workspace = torch.empty((_lib.rmsnorm_residual_bwd_workspace_size(R, Cc),), dtype=torch.uint8, device=z.device)
-    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1, "workspace must be a 1-D uint8 tensor")
-    _one_device(dy=dy, z=z, gamma=gamma, rstd=rstd, dres=dres, dz=dz, workspace=workspace)
-    dgamma = torch.empty((Cc,), dtype=torch.float32, device=z.device)
-    _check(_lib.rmsnorm_residual_bwd(_ptr(dy), dcode, _ptr(z), zcode, _ptr(gamma), _ptr(rstd), _ptr(dres), R, Cc,
-                                     _ptr(dz), _ptr(dgamma), _ptr(workspace), workspace.numel(), _stream()),
-           "rmsnorm_residual_bwd")
+    workspace = _workspace(workspace, _lib.rmsnorm_residual_bwd_workspace_size(R, Cc), z.device)
+    dgamma = torch.empty_like(gamma)
+    _check(_lib.rmsnorm_residual_bwd(
+        _device_ptr(dy, at, "dy"), dcode, _device_ptr(z, at, "z"), zcode, _device_ptr(gamma, at, "gamma"),
+        _device_ptr(rstd, at, "rstd"), _device_ptr(dres, at, "dres"), R, Cc, _device_ptr(dz, at, "dz"),
+        _device_ptr(dgamma, at, "dgamma"), _device_ptr(workspace, at, "workspace"), workspace.numel(),
+        _raw_stream(at)), "rmsnorm_residual_bwd")
     return dz, dgamma
 
 
@@ -709,13 +739,6 @@ def _ffn_weights(w13: torch.Tensor, w2: torch.Tensor, H: int) -> int:
     return F
 
 
-def _ffn_workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1, "workspace must be a 1-D uint8 tensor")
-    return workspace
-
-
 def swiglu_ffn_fwd(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, add: Optional[torch.Tensor] = None,
                    save_h13: bool = False, workspace: Optional[torch.Tensor] = None,
                    out: Optional[torch.Tensor] = None):
@@ -726,13 +749,16 @@ def swiglu_ffn_fwd(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, add: Op
     F = _ffn_weights(w13, w2, H)
     if add is not None:
         _tensor(add, (M, H), torch.bfloat16, "add")
-    workspace = _ffn_workspace(workspace, _lib.swiglu_ffn_fwd_workspace_size(M, H, F), x.device)
+    if out is not None:
+        _tensor(out, (M, H), torch.bfloat16, "out")
+    at = _device_of(x, "x")
+    workspace = _workspace(workspace, _lib.swiglu_ffn_fwd_workspace_size(M, H, F), x.device)
     out = torch.empty_like(x) if out is None else out
-    _tensor(out, (M, H), torch.bfloat16, "out")
-    _one_device(x=x, w13=w13, w2=w2, add=add, out=out, workspace=workspace)
     h13 = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=x.device) if save_h13 else None
-    _check(_lib.swiglu_ffn_fwd(_ptr(x), _ptr(w13), _ptr(w2), _ptr(add), M, H, F, _ptr(h13), _ptr(out),
-                               _ptr(workspace), workspace.numel(), _stream()), "swiglu_ffn_fwd")
+    _check(_lib.swiglu_ffn_fwd(
+        _device_ptr(x, at, "x"), _device_ptr(w13, at, "w13"), _device_ptr(w2, at, "w2"), _device_ptr(add, at, "add"), M,
+        H, F, _device_ptr(h13, at, "h13"), _device_ptr(out, at, "out"), _device_ptr(workspace, at, "workspace"),
+        workspace.numel(), _raw_stream(at)), "swiglu_ffn_fwd")
     return out, h13
 
 
@@ -748,19 +774,24 @@ def swiglu_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
     _tensor(x, (M, H), torch.bfloat16, "x")
     _tensor(h13, (M, 2 * F), torch.bfloat16, "h13")
     _need(dw_dtype in (torch.bfloat16, torch.float32), "dw_dtype must be bf16 or fp32")
-    workspace = _ffn_workspace(workspace, _lib.swiglu_ffn_bwd_workspace_size(M, H, F), x.device)
-    dx = torch.empty_like(x) if flags & BWD_DGRAD else None
-    if flags & BWD_WGRAD:
-        dw13 = torch.empty((2 * F, H), dtype=dw_dtype, device=x.device) if dw13 is None else dw13
-        dw2 = torch.empty((H, F), dtype=dw_dtype, device=x.device) if dw2 is None else dw2
+    wgrad = bool(flags & BWD_WGRAD)
+    _need(wgrad or (dw13 is None and dw2 is None), "dw13 and dw2 need BWD_WGRAD")
+    if dw13 is not None:
         _tensor(dw13, (2 * F, H), dw_dtype, "dw13")
+    if dw2 is not None:
         _tensor(dw2, (H, F), dw_dtype, "dw2")
-    else:
-        _need(dw13 is None and dw2 is None, "dw13 and dw2 need BWD_WGRAD")
-    _one_device(dy=dy, x=x, w13=w13, w2=w2, h13=h13, dw13=dw13, dw2=dw2, workspace=workspace)
-    _check(_lib.swiglu_ffn_bwd(_ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(h13), M, H, F, flags, _ptr(dx),
-                               _ptr(dw13), _ptr(dw2), DTYPE_F32 if dw_dtype == torch.float32 else DTYPE_BF16,
-                               _ptr(workspace), workspace.numel(), _stream()), "swiglu_ffn_bwd")
+    at = _device_of(dy, "dy")
+    dev = dy.device
+    workspace = _workspace(workspace, _lib.swiglu_ffn_bwd_workspace_size(M, H, F), dev)
+    dx = torch.empty_like(x) if flags & BWD_DGRAD else None
+    if wgrad:
+        dw13 = torch.empty((2 * F, H), dtype=dw_dtype, device=dev) if dw13 is None else dw13
+        dw2 = torch.empty((H, F), dtype=dw_dtype, device=dev) if dw2 is None else dw2
+    _check(_lib.swiglu_ffn_bwd(
+        _device_ptr(dy, at, "dy"), _device_ptr(x, at, "x"), _device_ptr(w13, at, "w13"), _device_ptr(w2, at, "w2"),
+        _device_ptr(h13, at, "h13"), M, H, F, flags, _device_ptr(dx, at, "dx"), _device_ptr(dw13, at, "dw13"),
+        _device_ptr(dw2, at, "dw2"), DTYPE_F32 if dw_dtype == torch.float32 else DTYPE_BF16,
+        _device_ptr(workspace, at, "workspace"), workspace.numel(), _raw_stream(at)), "swiglu_ffn_bwd")
     return dx, dw13, dw2
 
 
@@ -859,10 +890,12 @@ def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int,
             _need(v.dtype == dt and v.numel() == 1, f"{name} must be one value of {dt}")
             dev[name] = v
     _need(grad_scale is None or "grad_scale" in dev, "grad_scale must be a device tensor")
-    _one_device(table=plan.table, **dev)
-    _check(_lib.adamw_step(_ptr(plan.table), plan.chunks, plan.state_bits, 0.0 if "lr" in dev else lr, beta1, beta2, eps,
-                           1 if "step" in dev else step, _ptr(dev.get("lr")), _ptr(dev.get("step")),
-                           _ptr(dev.get("grad_scale")), seed, rng_stream & 0xFFFFFFFF, _stream()), "adamw_step")
+    at = _device_of(plan.table, "the plan")
+    _check(_lib.adamw_step(
+        _device_ptr(plan.table, at, "the plan"), plan.chunks, plan.state_bits, 0.0 if "lr" in dev else lr, beta1, beta2,
+        eps, 1 if "step" in dev else step, _device_ptr(dev.get("lr"), at, "lr"), _device_ptr(dev.get("step"), at, "step"),
+        _device_ptr(dev.get("grad_scale"), at, "grad_scale"), seed, rng_stream & 0xFFFFFFFF, _raw_stream(at)),
+        "adamw_step")
 
 
 # ---- measurement kernels of include/pmn_probe.h ---------------------------------------------

@@ -12,11 +12,13 @@
 // dgrad, both operands in wgrad).
 //
 // Operands stream through a ring of LDS stages of 32 k, filled by buffer_load ... lds (global -> LDS
-// without registers), 1 KB pieces dealt evenly to the wavefronts, so "stage s has landed" is the
-// per-wavefront condition vmcnt <= pieces issued after it, followed by a barrier. A wavefront reads the
-// fragments of stage v + 1 while the MFMAs of stage v run from registers. Bounds are the buffer
-// descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
-// the same code.
+// without registers), 1 KB pieces dealt evenly to the wavefronts. Two stages are filled together, a
+// piece's two halves one after the other: a row of a k-contiguous operand gives 64 bytes to a stage,
+// and the second half of the 128-byte line then comes from the first-level cache instead of a second
+// time from L2. "The pair has landed" is the per-wavefront condition vmcnt <= loads issued after it,
+// followed by a barrier. A wavefront reads the fragments of stage v + 1 while the MFMAs of stage v run
+// from registers. Bounds are the buffer descriptor's: rows and k past the operand read as zeros, so
+// every size that is a multiple of 8 runs the same code.
 //   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
 //     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured).
 //   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
@@ -57,23 +59,37 @@ struct FfnArgs {
     int SM, SN;
 };
 
-// 8 consecutive outputs n .. n+7 of output row c from their fp32 sums (SWIGLU: v = h1, v2 = h3 of
-// features n .. n+7). aux is read and out written only here, so out may be aux itself.
+// The 16-byte words of aux that 8 consecutive outputs n .. n+7 of output row c need: ADD's add, or
+// SWIGLU_BWD's h1 and h3.
 template <int EPI>
-PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], float (&v2)[8])
+PMN_DEV void ffn_aux8(const FfnArgs& p, int64_t c, int64_t n, uint4 (&w)[2])
+{
+    if (EPI == FFN_SWIGLU_BWD) {
+        w[0] = *reinterpret_cast<const uint4*>(p.aux + c * 2 * p.F + n);
+        w[1] = *reinterpret_cast<const uint4*>(p.aux + c * 2 * p.F + p.F + n);
+    } else if (EPI == FFN_ADD) {
+        w[0] = p.aux ? *reinterpret_cast<const uint4*>(p.aux + c * p.Nr + n) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+PMN_DEV void bf16x8_values(const uint4 w, float (&o)[8])
+{
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        o[2 * q] = bf16_lo(a[q]);
+        o[2 * q + 1] = bf16_hi(a[q]);
+    }
+}
+
+// 8 consecutive outputs n .. n+7 of output row c from their fp32 sums (SWIGLU: v = h1, v2 = h3 of
+// features n .. n+7) and their words of aux, read earlier by the same thread: out may be aux itself.
+template <int EPI>
+PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], float (&v2)[8], const uint4 (&aux)[2])
 {
     auto put = [](uint16_t* dst, const float (&o)[8]) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]),
                                                     bf16x2_bits(o[4], o[5]), bf16x2_bits(o[6], o[7]));
-    };
-    auto get = [](const uint16_t* src, float (&o)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src);
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            o[2 * q] = bf16_lo(a[q]);
-            o[2 * q + 1] = bf16_hi(a[q]);
-        }
     };
     if (EPI == FFN_SWIGLU) {
         float a[8];
@@ -86,8 +102,8 @@ PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], 
         }
     } else if (EPI == FFN_SWIGLU_BWD) {
         float h1[8], h3[8], a[8];
-        get(p.aux + c * 2 * p.F + n, h1);
-        get(p.aux + c * 2 * p.F + p.F + n, h3);
+        bf16x8_values(aux[0], h1);
+        bf16x8_values(aux[1], h3);
 #pragma unroll
         for (int u = 0; u < 8; u++) {
             // silu'(h) = s (1 + h (1 - s)); the values are rounded to bf16, far coarser than the
@@ -105,9 +121,9 @@ PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], 
         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        if (EPI == FFN_ADD && p.aux) {
+        if (EPI == FFN_ADD) {
             float b[8];
-            get(p.aux + c * p.Nr + n, b);
+            bf16x8_values(aux[0], b);
 #pragma unroll
             for (int u = 0; u < 8; u++) v[u] += b[u];
         }
@@ -134,30 +150,31 @@ PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
 
 constexpr uint32_t FFN_OUTSIDE = 0x80000000u;   // a buffer offset past every descriptor
 
-// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages
-template <int WR_, int WC_, int RB_, int CB_, int NST_>
+// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST slots of SK stages of 32 k, the
+// stages of a slot multiplied between two barriers
+template <int WR_, int WC_, int RB_, int CB_, int NST_, int SK_ = 1>
 struct FfnTile {
-    static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
+    static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_, SK = SK_;
     static constexpr int BR = WR * RB * 32, BC = WC * CB * 32;
     static constexpr int THREADS = WR * WC * 64;
     static constexpr int RBYTES = BR * 64, STAGE = (BR + BC) * 64;
-    static constexpr int PIECES = STAGE / 1024, PPW = PIECES / (WR * WC), RPIECES = RBYTES / 1024;
+    static constexpr int RPW = BR / 16 / (WR * WC), CPW = BC / 16 / (WR * WC), PPW = RPW + CPW;   // pieces per wavefront
     static constexpr int OPITCH = BR + 4;                       // floats per staged output row
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
-    static constexpr int RING = NST * STAGE, OUTB = OROWS * OPITCH * 4;
+    static constexpr int RING = NST * SK * STAGE, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
-    static_assert(PIECES % (WR * WC) == 0, "every wavefront loads the same number of pieces");
-    static_assert((NST - 2) * PPW <= 63, "vmcnt");
+    static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
+    static_assert((NST - 1) * SK * PPW <= 63, "vmcnt");
 };
 
 template <typename T, bool RKC, bool CKC, int EPI>
-__global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(FfnArgs p)
+__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn_gemm(FfnArgs p)
 {
-    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, PPW = T::PPW;
+    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, SK = T::SK, PPW = T::PPW;
     constexpr bool SWI = EPI == FFN_SWIGLU;
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
-    if (RB == 4) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
+    if (RB * CB == 16) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / T::WC, wc = wave % T::WC, l32 = lane & 31, hh = lane >> 5;
@@ -179,15 +196,14 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
     const int64_t s1 = EPI == FFN_PART ? KT * (split + 1) / p.splits : KT;
     const int nst = (int)(s1 - s0);
 
-    // this wavefront's pieces: byte offset of the lane's 16 bytes from the stage's first k, and for a
-    // k-contiguous operand the lane's first k of the stage
+    // This wavefront's pieces, RPW of R and then CPW of C: byte offset of the lane's 16 bytes from the
+    // operand's first at the stage, and for a k-contiguous operand the lane's first k of the stage.
     uint32_t voff[PPW];
     int kch[PPW];
 #pragma unroll
     for (int i = 0; i < PPW; i++) {
-        const int pc = wave * PPW + i;
-        const bool isr = pc < T::RPIECES;
-        const int q = isr ? pc : pc - T::RPIECES;
+        const bool isr = i < T::RPW;
+        const int q = isr ? wave * T::RPW + i : wave * T::CPW + i - T::RPW;
         const int64_t ld = isr ? p.ldr : p.ldc;
         if (isr ? RKC : CKC) {
             const int t = q * 16 + (lane >> 2);                       // tile row
@@ -214,41 +230,58 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
-    const uint32_t ldst = lds0 + wave * PPW * 1024;
-    // descriptor of an operand at stage s of this part (nothing past its last stage)
-    auto rsrc_at = [&](bool isr, int s) {
-        const uint16_t* base = isr ? p.r : p.c;
-        const int64_t ld = isr ? p.ldr : p.ldc, k0 = (s0 + s) * 32;
-        const bool kc = isr ? RKC : CKC;
-        if (kc) return buffer_of(base + (isr ? r0 : c0) * ld + k0, s < nst ? (int64_t)0x7FFFFFFF : 0);
-        return buffer_of(base + k0 * ld + (isr ? r0 : c0), s < nst ? ((p.K - k0) * ld - (isr ? r0 : c0)) * 2 : 0);
+    const uint32_t rdst = lds0 + wave * T::RPW * 1024, cdst = lds0 + T::RBYTES + wave * T::CPW * 1024;
+    // An operand's bytes from its first at stage 0 of this part, a stage's advance and how many bytes
+    // there are (a k-contiguous operand is bounded by rows and chunks instead)
+    struct Operand {
+        const uint8_t* base;
+        int64_t step, bytes;
     };
+    auto operand = [&](const uint16_t* src, bool kc, int64_t ld, int64_t at) {
+        const int64_t k0 = s0 * 32;
+        Operand o;
+        o.base = reinterpret_cast<const uint8_t*>(kc ? src + at * ld + k0 : src + k0 * ld + at);
+        o.step = kc ? 64 : 64 * ld;
+        o.bytes = kc ? INT64_MAX : ((p.K - k0) * ld - at) * 2;
+        return o;
+    };
+    const Operand opr = operand(p.r, RKC, p.ldr, r0), opc = operand(p.c, CKC, p.ldc, c0);
+    const int64_t w3_bytes = SWI ? p.F * p.ldr * 2 : 0;
     struct Stage {
-        i32x4 rr, rc, r3;
-        int left;
+        i32x4 r, r3, c;   // r3: the rows of w3
+        int left;         // k of this stage, at most 32
         uint32_t dst;
     };
     auto stage_at = [&](int s) {
         Stage g;
-        g.rr = rsrc_at(true, s);
-        g.rc = rsrc_at(false, s);
-        if (SWI) g.r3 = buffer_of(p.r + (p.F + r0) * p.ldr + (s0 + s) * 32, s < nst ? (int64_t)0x7FFFFFFF : 0);
+        const bool in = s < nst;   // nothing past the part's last stage
+        g.r = buffer_of(opr.base + s * opr.step, in ? opr.bytes - s * opr.step : 0);
+        if (SWI) g.r3 = buffer_of(opr.base + w3_bytes + s * opr.step, in ? opr.bytes - s * opr.step : 0);
+        g.c = buffer_of(opc.base + s * opc.step, in ? opc.bytes - s * opc.step : 0);
         const int64_t left = p.K - (s0 + s) * 32;
         g.left = left > 32 ? 32 : (int)left;
-        g.dst = ldst + (uint32_t)(s % NST) * T::STAGE;
+        g.dst = (uint32_t)(s % (NST * SK)) * T::STAGE;
         return g;
     };
     auto issue_piece = [&](const Stage& g, int i) {
-        const int pc = wave * PPW + i;
-        const bool isr = pc < T::RPIECES;
-        const bool w3 = SWI && isr && (pc >> 1) % RB >= RB / 2;
+        const bool isr = i < T::RPW;
         // chunks past K of a k-contiguous operand
         const uint32_t v = (isr ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i];
-        dma16_buffer(w3 ? g.r3 : (isr ? g.rr : g.rc), v, g.dst + i * 1024);
+        if (!isr) {
+            dma16_buffer(g.c, v, g.dst + cdst + (i - T::RPW) * 1024);
+        } else if (!SWI) {
+            dma16_buffer(g.r, v, g.dst + rdst + i * 1024);
+        } else {
+            const bool w3 = ((wave * T::RPW + i) >> 1) % RB >= RB / 2;
+            i32x4 d;
+#pragma unroll
+            for (int q = 0; q < 4; q++) d[q] = __builtin_amdgcn_readfirstlane(w3 ? g.r3[q] : g.r[q]);
+            dma16_buffer(d, v, g.dst + rdst + i * 1024);
+        }
     };
 
     struct Frags {
-        bf16x8 r[RB][2], c[CB][2];
+        bf16x8 r[RB][2 * SK], c[CB][2 * SK];
     };
     // lane constants of the fragment reads
     const int swz = (l32 >> 2) & 3;
@@ -265,11 +298,12 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
     };
-    constexpr int NREAD = 2 * (RB + CB);
-    auto read_one = [&](const uint8_t* base, int n, Frags& f) {
+    constexpr int NREAD = 2 * SK * (RB + CB);   // fragments of a slot, in the order of their use
+    auto read_one = [&](const uint8_t* slot, int n, Frags& f) {
         const int ks = n / (RB + CB), b = n % (RB + CB);
-        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks);
-        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks);
+        const uint8_t* base = slot + (ks >> 1) * T::STAGE;
+        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks & 1);
+        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks & 1);
     };
 
     f32x16 acc[RB][CB];
@@ -280,47 +314,70 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // One step: stage v + 1 has landed and every wavefront is done reading stage v, whose slot is
-    // refilled with stage v + NST. The step's loads and fragment reads are spread over its MFMAs.
-    constexpr int NM = 2 * RB * CB, NA = PPW + NREAD;
+    // One step: slot v + 1 has landed and every wavefront is done reading slot v, which is refilled with
+    // the stages of slot v + NST. The loads are spread over the step's MFMAs and the fragment reads over
+    // the first three quarters of them, so that the last have come back before the next step's barrier
+    // (in the last quarter, or with all loads first, a 256 x 256 tile's steps measured 4% slower).
+    constexpr int NM = 2 * SK * RB * CB, NL = SK * PPW, NRQ = NM * 3 / 4;
     auto step = [&](int v, const Frags& cur, Frags& nxt) {
-        wait_loads_and_barrier<(NST - 2) * PPW>();
-        const Stage g = stage_at(v + NST);
-        const uint8_t* rbase = lds + ((v + 1) % NST) * T::STAGE;
+        wait_loads_and_barrier<(NST - 2) * NL>();
+        Stage g = stage_at((v + NST) * SK);
+        const uint8_t* rbase = lds + ((v + 1) % NST) * (SK * T::STAGE);
 #pragma unroll
         for (int q = 0; q < NM; q++) {
             const int ks = q / (RB * CB), i = (q / CB) % RB, j = q % CB;
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cur.r[i][ks], cur.c[j][ks], acc[i][j], 0, 0, 0);
 #pragma unroll
-            for (int n = q * NA / NM; n < (q + 1) * NA / NM; n++) {
-                if (n < PPW) issue_piece(g, n);
-                else read_one(rbase, n - PPW, nxt);
+            for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
+#pragma unroll
+            for (int n = q * NL / NM; n < (q + 1) * NL / NM; n++) {
+                if (n > 0 && n % PPW == 0) g = stage_at((v + NST) * SK + n / PPW);
+                issue_piece(g, n % PPW);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     {
 #pragma unroll
-        for (int s = 0; s < NST; s++) {
+        for (int s = 0; s < NST * SK; s++) {
             const Stage g = stage_at(s);
 #pragma unroll
             for (int i = 0; i < PPW; i++) issue_piece(g, i);
         }
         Frags f0, f1;
-        wait_loads_and_barrier<(NST - 1) * PPW>();
+        wait_loads_and_barrier<(NST - 1) * NL>();
 #pragma unroll
         for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
-        for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
+        for (int v = 0; v * SK < nst; v += 2) {     // stages past the last multiply zeros
             step(v, f0, f1);
             step(v + 1, f1, f0);
         }
         wait_loads_and_barrier<0>();
     }
 
-    // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]
+    // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]; a thread finishes NP pieces
+    // of 8 values, whose words of aux are on their way while the rows are staged
     float* const ot = reinterpret_cast<float*>(lds);
+    constexpr int NW = (SWI ? BR / 2 : BR) / 8, NP = T::OROWS * NW / T::THREADS;
+    static_assert(T::OROWS * NW % T::THREADS == 0, "whole pieces per thread");
+    auto place = [&](int j, int k, int& rr, int& n, int64_t& c) {
+        const int at = k * T::THREADS + tid;
+        rr = at / NW;
+        n = (at % NW) * 8;
+        c = c0 + (rr >> 5) * (32 * CB) + j * 32 + (rr & 31);
+        return c < p.Nc && r0 + n < (SWI ? p.F : p.Nr);
+    };
 #pragma unroll
     for (int j = 0; j < CB; j++) {
+        uint4 aux[NP][2];
+        if (EPI == FFN_ADD || EPI == FFN_SWIGLU_BWD) {
+#pragma unroll
+            for (int k = 0; k < NP; k++) {
+                int rr, n;
+                int64_t c;
+                if (place(j, k, rr, n, c)) ffn_aux8<EPI>(p, c, r0 + n, aux[k]);
+            }
+        }
         if (j > 0) __syncthreads();
         float* const row = ot + (wc * 32 + l32) * T::OPITCH;
 #pragma unroll
@@ -334,11 +391,11 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
-        constexpr int NW = (SWI ? BR / 2 : BR) / 8;                 // 8-value pieces of a staged row
-        for (int k = tid; k < T::OROWS * NW; k += T::THREADS) {
-            const int rr = k / NW, n = (k % NW) * 8;
-            const int64_t c = c0 + (rr >> 5) * (32 * CB) + j * 32 + (rr & 31);
-            if (c >= p.Nc || r0 + n >= (SWI ? p.F : p.Nr)) continue;
+#pragma unroll
+        for (int k = 0; k < NP; k++) {
+            int rr, n;
+            int64_t c;
+            if (!place(j, k, rr, n, c)) continue;
             const float* src = ot + rr * T::OPITCH + n;
             float v[8], v2[8];
 #pragma unroll
@@ -355,7 +412,7 @@ __global__ __launch_bounds__(T::THREADS, T::RB == 4 ? 1 : 2) void k_ffn_gemm(Ffn
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             } else {
-                ffn_finish8<EPI>(p, c, r0 + n, v, v2);
+                ffn_finish8<EPI>(p, c, r0 + n, v, v2, aux[k]);
             }
         }
     }
@@ -370,6 +427,8 @@ __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
     if (i >= p.Nc * per) return;
     const int64_t c = i / per, n = (i - c * per) * 8;
     float v[8], v2[8];
+    uint4 aux[2];
+    ffn_aux8<EPI>(p, c, n, aux);
     auto sum = [&](int64_t col, float (&o)[8]) {
 #pragma unroll
         for (int u = 0; u < 8; u++) o[u] = 0.0f;
@@ -383,12 +442,134 @@ __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
     };
     sum(n, v);
     if (EPI == FFN_SWIGLU) sum(p.F + n, v2);
-    ffn_finish8<EPI>(p, c, n, v, v2);
+    ffn_finish8<EPI>(p, c, n, v, v2, aux);
+}
+
+// A product for few output rows (Nc <= 16 NT, both operands k-contiguous): the R operand, the weights,
+// streams once from HBM and bounds it. A workgroup holds 16 rows of R (SWIGLU: 8 features of w1 and
+// the same of w3) and its 8 wavefronts share the contraction in units of 64 k, one 128-byte line of
+// each row, dealt in turn so that together they walk the rows; operands go straight to registers of
+// v_mfma_f32_16x16x32_bf16 and the wavefronts' sums are added in order through LDS: one launch, no
+// workspace. Columns past Nc repeat the last row and are not stored.
+#ifndef X_W
+#define X_W 8
+#endif
+#ifndef X_U
+#define X_U 4
+#endif
+template <int NT, int EPI>
+__global__ __launch_bounds__(X_W * 64, X_W >= 16 ? 1 : 2) void k_ffn_few(FfnArgs p)
+{
+    constexpr bool SWI = EPI == FFN_SWIGLU;
+    constexpr int W = X_W;
+    constexpr int U = X_U;   // units loaded ahead of their products
+    __shared__ float4 red[W][NT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    const int64_t r0 = (int64_t)blockIdx.x * (SWI ? 8 : 16);
+    int64_t row = SWI ? r0 + (l16 & 7) : r0 + l16;
+    const int64_t rows = SWI ? p.F : p.Nr;
+    row = row < rows ? row : rows - 1;
+    if (SWI && l16 >= 8) row += p.F;
+    const uint16_t* const rp = p.r + row * p.ldr + 8 * g;
+    const uint16_t* cp[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        const int64_t c = 16 * t + l16;
+        cp[t] = p.c + (c < p.Nc ? c : p.Nc - 1) * p.ldc + 8 * g;
+    }
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t units = p.K >> 6;
+    auto load = [](const uint16_t* q) { return *reinterpret_cast<const bf16x8*>(q); };
+#ifdef X_NT
+    auto loadw = [](const uint16_t* q) { typedef uint32_t u4 __attribute__((ext_vector_type(4))); return __builtin_bit_cast(bf16x8, __builtin_nontemporal_load(reinterpret_cast<const u4*>(q))); };
+#else
+    auto loadw = load;
+#endif
+    // U units from unit u on; CHECKED: chunks past K are zeros
+    auto batch = [&](int64_t u, auto checked) {
+        bf16x8 a[U][2], b[U][2][NT];
+#pragma unroll
+        for (int i = 0; i < U; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t k = (u + W * i) * 64 + 32 * h;
+                if (!decltype(checked)::value || k + 8 * g < p.K) {
+                    a[i][h] = loadw(rp + k);
+#pragma unroll
+                    for (int t = 0; t < NT; t++) b[i][h][t] = load(cp[t] + k);
+                } else {
+                    a[i][h] = bf16x8{};
+#pragma unroll
+                    for (int t = 0; t < NT; t++) b[i][h][t] = bf16x8{};
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < U; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h], b[i][h][t], acc[t], 0, 0, 0);
+    };
+    int64_t u = wave;
+    for (; u + W * (U - 1) < units; u += W * U) batch(u, std::false_type{});
+    for (; u * 64 < p.K; u += W * U) batch(u, std::true_type{});
+#pragma unroll
+    for (int t = 0; t < NT; t++) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+    if (wave >= NT) return;
+    // wavefront t finishes columns 16 t .. : lane l holds rows 4 (l / 16) .. +3 of column l % 16
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+        const float4 s = red[w][wave][lane];
+        v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
+    }
+    const int64_t c = 16 * wave + l16;
+    auto put = [](uint16_t* dst, const float (&o)[4]) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
+    };
+    if (SWI) {
+        // lanes 0 .. 31 hold h1 of 8 features, lanes 32 .. 63 their h3
+        float h3[4], a[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            h3[i] = __shfl_xor(v[i], 32, 64);
+            a[i] = silu(v[i]) * h3[i];
+        }
+        const int64_t f = r0 + 4 * g;
+        if (g >= 2 || c >= p.Nc || f >= p.F) return;
+        put(static_cast<uint16_t*>(p.out) + c * p.F + f, a);
+        if (p.out2) {
+            put(p.out2 + c * 2 * p.F + f, v);
+            put(p.out2 + c * 2 * p.F + p.F + f, h3);
+        }
+    } else {
+        const int64_t n = r0 + 4 * g;
+        if (c >= p.Nc || n >= p.Nr) return;
+        if (p.aux) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p.aux + c * p.Nr + n);
+            v[0] += bf16_lo(w.x); v[1] += bf16_hi(w.x); v[2] += bf16_lo(w.y); v[3] += bf16_hi(w.y);
+        }
+        put(static_cast<uint16_t*>(p.out) + c * p.Nr + n, v);
+    }
 }
 
 typedef FfnTile<2, 2, 4, 4, 4> FfnLarge;    // 256 x 256, one workgroup per CU
-typedef FfnTile<2, 2, 2, 2, 4> FfnMid;      // 128 x 128
-typedef FfnTile<4, 1, 1, 2, 6> FfnFew;      // 128 x 64: few output rows, the R operand streams
+#ifndef X_MID
+#define X_MID 2,2,2,2,4
+#endif
+typedef FfnTile<X_MID> FfnMid;      // 128 x 128
+#ifndef X_FEWT
+#define X_FEWT 4,1,1,2,5
+#endif
+#ifndef X_FW
+#define X_FW 1
+#endif
+typedef FfnTile<X_FEWT> FfnFew;      // 128 x 64: few output rows, the R operand streams
 
 constexpr int FFN_CUS = 256;   // the split's target; fixed, so that results depend on the sizes alone
 
@@ -409,11 +590,17 @@ static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
         s = s > most ? most : s;
         return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
     };
-    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), 2 * FFN_CUS, 8)};
+    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), X_FW * FFN_CUS, 8)};
     if (tiles(256, 256) >= 160) return {0, 0};
     const int64_t t = tiles(128, 128);
     if (t >= FFN_CUS || stages < 32) return {1, 0};
-    const int s = split_for(t, 2 * FFN_CUS, 16);
+    #ifndef X_MW
+#define X_MW 512
+#endif
+#ifndef X_ML
+#define X_ML 16
+#endif
+    const int s = split_for(t, X_MW, X_ML);
     return {1, s > 1 ? s : 0};
 }
 
@@ -441,6 +628,19 @@ static void ffn_launch_tile(FfnArgs p, hipStream_t stream)
 template <bool RKC, bool CKC, int EPI>
 static void ffn_gemm(FfnArgs p, float* part, hipStream_t stream)
 {
+#ifndef X_FEW
+#define X_FEW 16
+#endif
+    if constexpr (RKC && CKC) {
+        if (p.Nc <= X_FEW) {
+            const unsigned grid = (unsigned)(EPI == FFN_SWIGLU ? (p.F + 7) / 8 : (p.Nr + 15) / 16);
+            if (p.Nc <= 16) hipLaunchKernelGGL((k_ffn_few<1, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
+            else if (p.Nc <= 32) hipLaunchKernelGGL((k_ffn_few<2, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
+            else if (p.Nc <= 48) hipLaunchKernelGGL((k_ffn_few<3, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
+            else hipLaunchKernelGGL((k_ffn_few<4, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
+            return;
+        }
+    }
     const FfnPlan pl = ffn_plan(p.Nc, p.Nr, p.K, CKC);
     p.splits = pl.splits;
     p.part = part;

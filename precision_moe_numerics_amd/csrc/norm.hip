@@ -224,21 +224,24 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_bwd(
     }
 }
 
-// dgamma[c] = sum of the P partial rows: 64 columns a workgroup, 16 wavefronts over the rows.
+// dgamma[c] = sum of the P partial rows: 32 columns a workgroup (a 128-byte line of each row), 32
+// threads down the rows of each column, their sums added in order.
 __global__ __launch_bounds__(1024) void k_rmsnorm_dgamma(const float* __restrict__ part, int P, int C,
                                                          float* __restrict__ dgamma)
 {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    __shared__ float red[32][33];
+    const int x = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + x;
     float s = 0.0f;
-    if (c < C)
-        for (int p = w; p < P; p += 16) s += part[(int64_t)p * C + c];
-    red[w][lane] = s;
+    if (c < C) {
+#pragma unroll 8
+        for (int p = w; p < P; p += 32) s += part[(int64_t)p * C + c];
+    }
+    red[w][x] = s;
     __syncthreads();
     if (w == 0 && c < C) {
 #pragma unroll
-        for (int i = 1; i < 16; i++) s += red[i][lane];
+        for (int i = 1; i < 32; i++) s += red[i][x];
         dgamma[c] = s;
     }
 }
@@ -338,7 +341,7 @@ hipError_t launch_rmsnorm_bwd(const void* dy, bool dy_f32, const void* z, bool z
     else if (dy_f32) PMN_TYPED(uint16_t, float);
     else PMN_TYPED(uint16_t, uint16_t);
 #undef PMN_TYPED
-    hipLaunchKernelGGL(k_rmsnorm_dgamma, dim3((unsigned)((C + 63) / 64)), dim3(1024), 0, stream, part,
+    hipLaunchKernelGGL(k_rmsnorm_dgamma, dim3((unsigned)((C + 31) / 32)), dim3(1024), 0, stream, part,
                        (int)rmsnorm_bwd_groups(rows, C), (int)C, dgamma);
     return hipGetLastError();
 }
