@@ -56,7 +56,6 @@ struct FfnArgs {
     float* part;            // PART: [splits x Nc x Nr]
     int splits;
     int64_t rtiles, ctiles;
-    int SM, SN;
 };
 
 // The 16-byte words of aux that 8 consecutive outputs n .. n+7 of output row c need: ADD's add, or
@@ -150,47 +149,48 @@ PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
 
 constexpr uint32_t FFN_OUTSIDE = 0x80000000u;   // a buffer offset past every descriptor
 
-// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST slots of SK stages of 32 k, the
-// stages of a slot multiplied between two barriers
-template <int WR_, int WC_, int RB_, int CB_, int NST_, int SK_ = 1>
+// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages
+template <int WR_, int WC_, int RB_, int CB_, int NST_>
 struct FfnTile {
-    static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_, SK = SK_;
+    static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
     static constexpr int BR = WR * RB * 32, BC = WC * CB * 32;
     static constexpr int THREADS = WR * WC * 64;
     static constexpr int RBYTES = BR * 64, STAGE = (BR + BC) * 64;
     static constexpr int RPW = BR / 16 / (WR * WC), CPW = BC / 16 / (WR * WC), PPW = RPW + CPW;   // pieces per wavefront
     static constexpr int OPITCH = BR + 4;                       // floats per staged output row
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
-    static constexpr int RING = NST * SK * STAGE, OUTB = OROWS * OPITCH * 4;
+    static constexpr int RING = NST * STAGE, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
-    static_assert((NST - 1) * SK * PPW <= 63, "vmcnt");
+    static_assert((NST - 1) * PPW <= 63, "vmcnt");
 };
 
-template <typename T, bool RKC, bool CKC, int EPI>
-__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn_gemm(FfnArgs p)
+// Tile i of a product's rtiles x ctiles for workgroup L: workgroups L, L + 8, .. run on one XCD and take
+// consecutive tiles, in bands of 8 tile rows walked down their columns, so that the 32 tiles of an XCD at
+// a time share 8 + 4 operand panels in its L2. False past the last tile.
+PMN_DEV bool ffn_tile_of(const FfnArgs& p, int64_t L, int64_t& trow, int64_t& tcol)
 {
-    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, SK = T::SK, PPW = T::PPW;
+    const int64_t total = p.rtiles * p.ctiles, per = (total + 7) >> 3;
+    const int64_t i = (L & 7) * per + (L >> 3);
+    if ((L >> 3) >= per || i >= total) return false;
+    const int64_t band = i / (8 * p.ctiles), in = i - band * 8 * p.ctiles;
+    const int64_t height = p.rtiles - band * 8 < 8 ? p.rtiles - band * 8 : 8;
+    tcol = in / height;
+    trow = band * 8 + (in - tcol * height);
+    return true;
+}
+
+// The tile (trow, tcol) of a product, or part `split` of its contraction (PART).
+template <typename T, bool RKC, bool CKC, int EPI>
+PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, uint8_t* lds)
+{
+    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, PPW = T::PPW;
     constexpr bool SWI = EPI == FFN_SWIGLU;
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
-    if (RB * CB == 16) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / T::WC, wc = wave % T::WC, l32 = lane & 31, hh = lane >> 5;
-
-    TileXY tile;
-    int64_t L = blockIdx.x;
-    int split = 0;
-    if (EPI == FFN_PART) {
-        split = (int)(L % p.splits);
-        L /= p.splits;
-        tile.row = L % p.rtiles;
-        tile.col = L / p.rtiles;
-    } else if (!xcd_tile(L, p.rtiles, p.ctiles, p.SM, p.SN, tile)) {
-        return;
-    }
-    const int64_t r0 = tile.row * (SWI ? BR / 2 : BR), c0 = tile.col * BC;
+    const int64_t r0 = trow * (SWI ? BR / 2 : BR), c0 = tcol * BC;
     const int64_t KT = (p.K + 31) >> 5;
     const int64_t s0 = EPI == FFN_PART ? KT * split / p.splits : 0;
     const int64_t s1 = EPI == FFN_PART ? KT * (split + 1) / p.splits : KT;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
         g.c = buffer_of(opc.base + s * opc.step, in ? opc.bytes - s * opc.step : 0);
         const int64_t left = p.K - (s0 + s) * 32;
         g.left = left > 32 ? 32 : (int)left;
-        g.dst = (uint32_t)(s % (NST * SK)) * T::STAGE;
+        g.dst = (uint32_t)(s % NST) * T::STAGE;
         return g;
     };
     auto issue_piece = [&](const Stage& g, int i) {
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
     };
 
     struct Frags {
-        bf16x8 r[RB][2 * SK], c[CB][2 * SK];
+        bf16x8 r[RB][2], c[CB][2];
     };
     // lane constants of the fragment reads
     const int swz = (l32 >> 2) & 3;
@@ -298,12 +298,11 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
     };
-    constexpr int NREAD = 2 * SK * (RB + CB);   // fragments of a slot, in the order of their use
-    auto read_one = [&](const uint8_t* slot, int n, Frags& f) {
+    constexpr int NREAD = 2 * (RB + CB);   // fragments of a stage, in the order of their use
+    auto read_one = [&](const uint8_t* base, int n, Frags& f) {
         const int ks = n / (RB + CB), b = n % (RB + CB);
-        const uint8_t* base = slot + (ks >> 1) * T::STAGE;
-        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks & 1);
-        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks & 1);
+        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks);
+        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks);
     };
 
     f32x16 acc[RB][CB];
@@ -314,15 +313,15 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // One step: slot v + 1 has landed and every wavefront is done reading slot v, which is refilled with
-    // the stages of slot v + NST. The loads are spread over the step's MFMAs and the fragment reads over
+    // One step: stage v + 1 has landed and every wavefront is done reading stage v, whose slot is
+    // refilled with stage v + NST. The loads are spread over the step's MFMAs and the fragment reads over
     // the first three quarters of them, so that the last have come back before the next step's barrier
-    // (in the last quarter, or with all loads first, a 256 x 256 tile's steps measured 4% slower).
-    constexpr int NM = 2 * SK * RB * CB, NL = SK * PPW, NRQ = NM * 3 / 4;
+    // (all loads before all reads measured 4% slower, loads of two stages at a time 15%).
+    constexpr int NM = 2 * RB * CB, NRQ = NM * 3 / 4;
     auto step = [&](int v, const Frags& cur, Frags& nxt) {
-        wait_loads_and_barrier<(NST - 2) * NL>();
-        Stage g = stage_at((v + NST) * SK);
-        const uint8_t* rbase = lds + ((v + 1) % NST) * (SK * T::STAGE);
+        wait_loads_and_barrier<(NST - 2) * PPW>();
+        const Stage g = stage_at(v + NST);
+        const uint8_t* rbase = lds + ((v + 1) % NST) * T::STAGE;
 #pragma unroll
         for (int q = 0; q < NM; q++) {
             const int ks = q / (RB * CB), i = (q / CB) % RB, j = q % CB;
@@ -330,25 +329,22 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
 #pragma unroll
             for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
 #pragma unroll
-            for (int n = q * NL / NM; n < (q + 1) * NL / NM; n++) {
-                if (n > 0 && n % PPW == 0) g = stage_at((v + NST) * SK + n / PPW);
-                issue_piece(g, n % PPW);
-            }
+            for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) issue_piece(g, n);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     {
 #pragma unroll
-        for (int s = 0; s < NST * SK; s++) {
+        for (int s = 0; s < NST; s++) {
             const Stage g = stage_at(s);
 #pragma unroll
             for (int i = 0; i < PPW; i++) issue_piece(g, i);
         }
         Frags f0, f1;
-        wait_loads_and_barrier<(NST - 1) * NL>();
+        wait_loads_and_barrier<(NST - 1) * PPW>();
 #pragma unroll
         for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
-        for (int v = 0; v * SK < nst; v += 2) {     // stages past the last multiply zeros
+        for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
             step(v, f0, f1);
             step(v + 1, f1, f0);
         }
@@ -418,6 +414,47 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
     }
 }
 
+template <typename T, bool RKC, bool CKC, int EPI>
+__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn_gemm(FfnArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+    if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
+    int64_t L = blockIdx.x, trow, tcol;
+    int split = 0;
+    if (EPI == FFN_PART) {
+        split = (int)(L % p.splits);
+        L /= p.splits;
+        trow = L % p.rtiles;
+        tcol = L / p.rtiles;
+    } else if (!ffn_tile_of(p, L, trow, tcol)) {
+        return;
+    }
+    ffn_tile<T, RKC, CKC, EPI>(p, trow, tcol, split, lds);
+}
+
+// The gradients' products in one launch, weight gradients and dx in any order: workgroups up to end[0]
+// work on p[0], up to end[1] on p[1], .. The chip stays full where one product's tiles run out, which
+// with a launch each costs every product its last, partly filled round.
+struct FfnGrads {
+    FfnArgs p[3];
+    uint32_t end[3];
+    int dx;   // which of them is dx
+};
+template <typename T, int DW>
+__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn_grads(FfnGrads a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+    if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));
+    const uint32_t L = blockIdx.x;
+    const int w = L < a.end[0] ? 0 : L < a.end[1] ? 1 : 2;
+    const uint32_t first = w == 0 ? 0u : w == 1 ? a.end[0] : a.end[1];
+    const FfnArgs& p = a.p[w];
+    int64_t trow, tcol;
+    if (!ffn_tile_of(p, L - first, trow, tcol)) return;
+    if (w == a.dx) ffn_tile<T, false, true, FFN_BF16>(p, trow, tcol, 0, lds);
+    else ffn_tile<T, false, false, DW>(p, trow, tcol, 0, lds);
+}
+
 // Finish a split product: the parts of 8 consecutive outputs added in order. One thread each.
 template <int EPI>
 __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
@@ -445,25 +482,21 @@ __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
     ffn_finish8<EPI>(p, c, n, v, v2, aux);
 }
 
-// A product for few output rows (Nc <= 16 NT, both operands k-contiguous): the R operand, the weights,
-// streams once from HBM and bounds it. A workgroup holds 16 rows of R (SWIGLU: 8 features of w1 and
-// the same of w3) and its 8 wavefronts share the contraction in units of 64 k, one 128-byte line of
-// each row, dealt in turn so that together they walk the rows; operands go straight to registers of
-// v_mfma_f32_16x16x32_bf16 and the wavefronts' sums are added in order through LDS: one launch, no
-// workspace. Columns past Nc repeat the last row and are not stored.
-#ifndef X_W
-#define X_W 8
-#endif
-#ifndef X_U
-#define X_U 4
-#endif
-template <int NT, int EPI>
-__global__ __launch_bounds__(X_W * 64, X_W >= 16 ? 1 : 2) void k_ffn_few(FfnArgs p)
+// A product for up to 16 output rows, both operands k-contiguous: the R operand, the weights, streams
+// once from HBM and bounds it. A workgroup holds 16 rows of R (SWIGLU: 8 features of w1 and the same of
+// w3) and its 8 wavefronts share the contraction in units of 64 k, one 128-byte line of each row, dealt
+// in turn so that together they walk the rows; operands go straight to registers of
+// v_mfma_f32_16x16x32_bf16, 4 units of a wavefront ahead, and the wavefronts' sums are added in order
+// through LDS: one launch, no workspace. Columns past Nc repeat the last row and are not stored. Each
+// workgroup reads all of C from L2, so beyond 16 rows the ring's tiles with a split contraction are
+// faster (32 rows of 7168 x 2048: 35 us, this kernel with two column tiles 42).
+// One row of 7168 x 2048 (88 MB of weights): 12 us and 8 us, 4.9 and 3.7 TB/s.
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void k_ffn_few(FfnArgs p)
 {
     constexpr bool SWI = EPI == FFN_SWIGLU;
-    constexpr int W = X_W;
-    constexpr int U = X_U;   // units loaded ahead of their products
-    __shared__ float4 red[W][NT][64];
+    constexpr int W = 8, U = 4;
+    __shared__ float4 red[W][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l16 = lane & 15, g = lane >> 4;
     const int64_t r0 = (int64_t)blockIdx.x * (SWI ? 8 : 16);
@@ -472,63 +505,46 @@ __global__ __launch_bounds__(X_W * 64, X_W >= 16 ? 1 : 2) void k_ffn_few(FfnArgs
     row = row < rows ? row : rows - 1;
     if (SWI && l16 >= 8) row += p.F;
     const uint16_t* const rp = p.r + row * p.ldr + 8 * g;
-    const uint16_t* cp[NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int64_t c = 16 * t + l16;
-        cp[t] = p.c + (c < p.Nc ? c : p.Nc - 1) * p.ldc + 8 * g;
-    }
-    f32x4 acc[NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint16_t* const cp = p.c + (l16 < p.Nc ? l16 : p.Nc - 1) * p.ldc + 8 * g;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t units = p.K >> 6;
     auto load = [](const uint16_t* q) { return *reinterpret_cast<const bf16x8*>(q); };
-#ifdef X_NT
-    auto loadw = [](const uint16_t* q) { typedef uint32_t u4 __attribute__((ext_vector_type(4))); return __builtin_bit_cast(bf16x8, __builtin_nontemporal_load(reinterpret_cast<const u4*>(q))); };
-#else
-    auto loadw = load;
-#endif
-    // U units from unit u on; CHECKED: chunks past K are zeros
+    // U units from unit u on; checked: chunks past K are zeros
     auto batch = [&](int64_t u, auto checked) {
-        bf16x8 a[U][2], b[U][2][NT];
+        bf16x8 a[U][2], b[U][2];
 #pragma unroll
         for (int i = 0; i < U; i++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int64_t k = (u + W * i) * 64 + 32 * h;
                 if (!decltype(checked)::value || k + 8 * g < p.K) {
-                    a[i][h] = loadw(rp + k);
-#pragma unroll
-                    for (int t = 0; t < NT; t++) b[i][h][t] = load(cp[t] + k);
+                    a[i][h] = load(rp + k);
+                    b[i][h] = load(cp + k);
                 } else {
                     a[i][h] = bf16x8{};
-#pragma unroll
-                    for (int t = 0; t < NT; t++) b[i][h][t] = bf16x8{};
+                    b[i][h] = bf16x8{};
                 }
             }
 #pragma unroll
         for (int i = 0; i < U; i++)
 #pragma unroll
             for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h], b[i][h][t], acc[t], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][h], b[i][h], acc, 0, 0, 0);
     };
     int64_t u = wave;
     for (; u + W * (U - 1) < units; u += W * U) batch(u, std::false_type{});
     for (; u * 64 < p.K; u += W * U) batch(u, std::true_type{});
-#pragma unroll
-    for (int t = 0; t < NT; t++) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    red[wave][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
-    if (wave >= NT) return;
-    // wavefront t finishes columns 16 t .. : lane l holds rows 4 (l / 16) .. +3 of column l % 16
+    if (wave > 0) return;
+    // lane l finishes rows 4 (l / 16) .. +3 of column l % 16
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < W; w++) {
-        const float4 s = red[w][wave][lane];
+        const float4 s = red[w][lane];
         v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
     }
-    const int64_t c = 16 * wave + l16;
+    const int64_t c = l16;
     auto put = [](uint16_t* dst, const float (&o)[4]) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
     };
@@ -559,17 +575,8 @@ __global__ __launch_bounds__(X_W * 64, X_W >= 16 ? 1 : 2) void k_ffn_few(FfnArgs
 }
 
 typedef FfnTile<2, 2, 4, 4, 4> FfnLarge;    // 256 x 256, one workgroup per CU
-#ifndef X_MID
-#define X_MID 2,2,2,2,4
-#endif
-typedef FfnTile<X_MID> FfnMid;      // 128 x 128
-#ifndef X_FEWT
-#define X_FEWT 4,1,1,2,5
-#endif
-#ifndef X_FW
-#define X_FW 1
-#endif
-typedef FfnTile<X_FEWT> FfnFew;      // 128 x 64: few output rows, the R operand streams
+typedef FfnTile<2, 2, 2, 2, 4> FfnMid;      // 128 x 128
+typedef FfnTile<4, 1, 1, 2, 4> FfnFew;      // 128 x 64: few output rows, the R operand streams
 
 constexpr int FFN_CUS = 256;   // the split's target; fixed, so that results depend on the sizes alone
 
@@ -590,17 +597,11 @@ static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
         s = s > most ? most : s;
         return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
     };
-    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), X_FW * FFN_CUS, 8)};
+    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), FFN_CUS, 8)};
     if (tiles(256, 256) >= 160) return {0, 0};
     const int64_t t = tiles(128, 128);
     if (t >= FFN_CUS || stages < 32) return {1, 0};
-    #ifndef X_MW
-#define X_MW 512
-#endif
-#ifndef X_ML
-#define X_ML 16
-#endif
-    const int s = split_for(t, X_MW, X_ML);
+    const int s = split_for(t, FFN_CUS, 16);
     return {1, s > 1 ? s : 0};
 }
 
@@ -609,35 +610,54 @@ static int64_t ffn_part_floats(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
     return (int64_t)ffn_plan(Nc, Nr, K, ckc).splits * Nc * Nr;
 }
 
-template <typename T, bool RKC, bool CKC, int EPI>
-static void ffn_launch_tile(FfnArgs p, hipStream_t stream)
+// Tile grid of a product; returns its workgroups (a multiple of 8, without PART)
+template <typename T, int EPI>
+static int64_t ffn_grid(FfnArgs& p)
 {
     const int64_t nr = EPI == FFN_SWIGLU ? p.F : p.Nr, br = EPI == FFN_SWIGLU ? T::BR / 2 : T::BR;
     p.rtiles = (nr + br - 1) / br;
     p.ctiles = (p.Nc + T::BC - 1) / T::BC;
-    int64_t grid;
-    if (EPI == FFN_PART) {
-        grid = p.rtiles * p.ctiles * p.splits;
-    } else {
-        xcd_shape(p.rtiles, p.ctiles, p.SM, p.SN);
-        grid = xcd_grid(p.rtiles, p.ctiles, p.SM, p.SN);
-    }
+    const int64_t n = p.rtiles * p.ctiles;
+    return EPI == FFN_PART ? n * p.splits : (n + 7) / 8 * 8;
+}
+
+template <typename T, bool RKC, bool CKC, int EPI>
+static void ffn_launch_tile(FfnArgs p, hipStream_t stream)
+{
+    const int64_t grid = ffn_grid<T, EPI>(p);
     hipLaunchKernelGGL((k_ffn_gemm<T, RKC, CKC, EPI>), dim3((unsigned)grid), dim3(T::THREADS), 0, stream, p);
+}
+
+// The gradients' products (count of them, dx at index dx or -1) in one launch, the longest contraction
+// first
+template <typename T, int DW>
+static void ffn_launch_grads(const FfnArgs* p, int count, int dx, hipStream_t stream)
+{
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < count; i++)
+        for (int j = i + 1; j < count; j++)
+            if (p[order[j]].K > p[order[i]].K) { const int t = order[i]; order[i] = order[j]; order[j] = t; }
+    FfnGrads a{};
+    a.dx = -1;
+    int64_t end = 0;
+    for (int i = 0; i < 3; i++) {
+        if (i < count) {
+            a.p[i] = p[order[i]];
+            if (order[i] == dx) a.dx = i;
+            end += ffn_grid<T, FFN_BF16>(a.p[i]);
+        }
+        a.end[i] = (uint32_t)end;
+    }
+    hipLaunchKernelGGL((k_ffn_grads<T, DW>), dim3((unsigned)end), dim3(T::THREADS), 0, stream, a);
 }
 
 template <bool RKC, bool CKC, int EPI>
 static void ffn_gemm(FfnArgs p, float* part, hipStream_t stream)
 {
-#ifndef X_FEW
-#define X_FEW 16
-#endif
     if constexpr (RKC && CKC) {
-        if (p.Nc <= X_FEW) {
+        if (p.Nc <= 16) {
             const unsigned grid = (unsigned)(EPI == FFN_SWIGLU ? (p.F + 7) / 8 : (p.Nr + 15) / 16);
-            if (p.Nc <= 16) hipLaunchKernelGGL((k_ffn_few<1, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
-            else if (p.Nc <= 32) hipLaunchKernelGGL((k_ffn_few<2, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
-            else if (p.Nc <= 48) hipLaunchKernelGGL((k_ffn_few<3, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
-            else hipLaunchKernelGGL((k_ffn_few<4, EPI>), dim3(grid), dim3(X_W * 64), 0, stream, p);
+            hipLaunchKernelGGL((k_ffn_few<EPI>), dim3(grid), dim3(512), 0, stream, p);
             return;
         }
     }
@@ -683,24 +703,63 @@ hipError_t launch_ffn_fwd(const uint16_t* x, const uint16_t* w13, const uint16_t
     return hipGetLastError();
 }
 
+// Tile of the gradients' one launch, -1 for a launch each with split contractions. One launch where
+// its workgroups fill the chip and the longest contraction is not much longer than their share of it:
+// with few tiles of a long one (small weights, many tokens) splitting them is faster.
+static int ffn_grads_tile(int64_t M, int64_t H, int64_t F, bool dgrad, bool wgrad)
+{
+    if (M == 0) return 1;
+    int64_t tiles[2] = {0, 0}, steps[2] = {0, 0}, longest = 0;
+    auto count = [&](int64_t nc, int64_t nr, int64_t k) {
+        const int64_t st = (k + 31) / 32;
+        longest = st > longest ? st : longest;
+        for (int i = 0; i < 2; i++) {
+            const int64_t b = i == 0 ? 256 : 128, t = ((nr + b - 1) / b) * ((nc + b - 1) / b);
+            tiles[i] += t;
+            steps[i] += t * st;
+        }
+    };
+    if (wgrad) {
+        count(2 * F, H, M);
+        count(H, F, M);
+    }
+    if (dgrad) count(M, H, 2 * F);
+    if (tiles[0] >= 640 && longest * FFN_CUS <= steps[0]) return 0;
+    if (tiles[1] >= FFN_CUS && longest * FFN_CUS <= steps[1]) return 1;
+    return -1;
+}
+
 // dh13 [M x 2F] and a [M x F] from dy, w2 and h13; then the gradients asked for
 hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
                           const uint16_t* h13, int64_t M, int64_t H, int64_t F, uint16_t* dh13, uint16_t* a,
                           float* part, uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream)
 {
     if (M > 0) ffn_gemm<false, true, FFN_SWIGLU_BWD>(FfnArgs{w2, dy, F, H, F, M, H, dh13, h13, a, F}, part, stream);
-    if (M > 0 && dx)
-        ffn_gemm<false, true, FFN_BF16>(FfnArgs{w13, dh13, H, 2 * F, H, M, 2 * F, dx, nullptr, nullptr, F}, part, stream);
+    FfnArgs g[3];
+    int count = 0, idx = -1;
     if (dw13) {
-        const FfnArgs g13{x, dh13, H, 2 * F, H, 2 * F, M, dw13, nullptr, nullptr, F};
-        const FfnArgs g2{a, dy, F, H, F, H, M, dw2, nullptr, nullptr, F};
-        if (dw_f32) {
-            ffn_gemm<false, false, FFN_F32>(g13, part, stream);
-            ffn_gemm<false, false, FFN_F32>(g2, part, stream);
+        g[count++] = FfnArgs{x, dh13, H, 2 * F, H, 2 * F, M, dw13, nullptr, nullptr, F};
+        g[count++] = FfnArgs{a, dy, F, H, F, H, M, dw2, nullptr, nullptr, F};
+    }
+    if (M > 0 && dx) {
+        idx = count;
+        g[count++] = FfnArgs{w13, dh13, H, 2 * F, H, M, 2 * F, dx, nullptr, nullptr, F};
+    }
+    const int tile = ffn_grads_tile(M, H, F, dx != nullptr, dw13 != nullptr);
+    if (tile >= 0) {
+        if (tile == 0) {
+            if (dw_f32) ffn_launch_grads<FfnLarge, FFN_F32>(g, count, idx, stream);
+            else ffn_launch_grads<FfnLarge, FFN_BF16>(g, count, idx, stream);
         } else {
-            ffn_gemm<false, false, FFN_BF16>(g13, part, stream);
-            ffn_gemm<false, false, FFN_BF16>(g2, part, stream);
+            if (dw_f32) ffn_launch_grads<FfnMid, FFN_F32>(g, count, idx, stream);
+            else ffn_launch_grads<FfnMid, FFN_BF16>(g, count, idx, stream);
         }
+        return hipGetLastError();
+    }
+    for (int i = 0; i < count; i++) {
+        if (i == idx) ffn_gemm<false, true, FFN_BF16>(g[i], part, stream);
+        else if (dw_f32) ffn_gemm<false, false, FFN_F32>(g[i], part, stream);
+        else ffn_gemm<false, false, FFN_BF16>(g[i], part, stream);
     }
     return hipGetLastError();
 }
