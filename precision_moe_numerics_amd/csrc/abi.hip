@@ -631,8 +631,9 @@ int adamw_step(const void* table, int64_t chunks, int state_bits, double lr, dou
     if (!table) return PMN_EINVAL;
     if (!aligned(table, 8) || !aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(grad_scale_dev, 4))
         return PMN_EALIGN;
+    const double bc1 = -std::expm1((double)step * std::log(beta1)), bc2 = -std::expm1((double)step * std::log(beta2));
     const pmn::AdamwScalars a{(float)lr, (float)beta1, (float)beta2, (float)(1.0 - beta1), (float)(1.0 - beta2),
-                              (float)eps, std::log(beta1), std::log(beta2), step, lr_dev, step_dev, grad_scale_dev,
+                              (float)eps, (float)(1.0 / bc1), (float)(1.0 / std::sqrt(bc2)), std::log(beta1), std::log(beta2), step, lr_dev, step_dev, grad_scale_dev,
                               seed, rng_stream};
     return status(pmn::launch_adamw(table, chunks, state_bits, a, hs(stream)));
 }

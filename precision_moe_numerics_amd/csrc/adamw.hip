@@ -25,7 +25,7 @@ namespace pmn {
 
 namespace adw {
 constexpr int THREADS = 256;
-constexpr int CHUNK = THREADS * 8;   // values per workgroup
+constexpr int CHUNK = THREADS * 8;   // values per workgroup (chunks of 4 and 8 times as many: 4% and 9% slower)
 }  // namespace adw
 
 int64_t adamw_chunk() { return adw::CHUNK; }
@@ -115,24 +115,35 @@ PMN_DEV void load_codes(const uint8_t* p, int n, float scale, float (&v)[8])
     }
 }
 
-// 8 values of a block whose 4 lanes call together: stochastic E4M3 codes, the quad's first lane
-// writes the E8M0 byte. POSITIVE: values >= 0, one above zero gets at least the smallest code.
-template <bool POSITIVE>
-PMN_DEV void store_codes(uint8_t* p, uint8_t* e8m0, int n, const float (&v)[8], uint64_t seed, uint32_t stream,
-                         uint64_t blk)
+// Lane L of each quad, in every lane of it
+template <int L>
+PMN_DEV float quad_lane(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x55 * L, 0xF, 0xF, true));
+}
+
+// Exponent of the E8M0 scale of a block held by the 4 lanes of a quad
+PMN_DEV int block_exponent(const float (&v)[8])
 {
     float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(v[j]));
-    const int e = e8m0_exponent<E8M0_E4M3>(quad_max4(amax));
+    return e8m0_exponent<E8M0_E4M3>(quad_max4(amax));
+}
+
+// 8 values of a block of exponent e: stochastic E4M3 codes of v * scale; the quad's first lane writes
+// the E8M0 byte. scale is 2^-e as torch.ldexp forms it, by powf, which for some e is one ulp low (never
+// high, so a block's largest value stays within 448): states packed by torch operations have the same
+// codes. POSITIVE: values >= 0, one above zero gets at least the smallest code.
+template <bool POSITIVE>
+PMN_DEV void store_codes(uint8_t* p, uint8_t* e8m0, int n, const float (&v)[8], int e, float scale, uint64_t seed,
+                         uint32_t stream, uint64_t blk)
+{
     uint32_t rw[4], w[2] = {0u, 0u};
     rand16x8(seed, stream, blk, rw);
-    // 2^-e as torch.ldexp forms it, by powf, which for some e is one ulp low (never high, so a block's
-    // largest value stays within 448): states packed by torch operations have the same codes
-    const float inv = powf(2.0f, (float)-e);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        uint32_t c = e4m3_sr(v[j] * inv, sr_operand(rw[j >> 1], j & 1));
+        uint32_t c = e4m3_sr(v[j] * scale, sr_operand(rw[j >> 1], j & 1));
         if (POSITIVE && v[j] > 0.0f && c == 0u) c = 1u;
         w[j >> 2] |= c << (8 * (j & 3));
     }
@@ -146,9 +157,15 @@ PMN_DEV void store_codes(uint8_t* p, uint8_t* e8m0, int n, const float (&v)[8], 
     if ((threadIdx.x & 3) == 0) *e8m0 = (uint8_t)(e + 127);
 }
 
+// 1 / (1 - beta1^t) and 1 / sqrt(1 - beta2^t): in fp64 on the host, or here for a step on the device
+PMN_DEV void bias_corrections(const AdamwScalars& a, int64_t step, float& ibc1, float& rsbc2)
+{
+    ibc1 = (float)(-1.0 / expm1((double)step * a.ln_beta1));
+    rsbc2 = (float)(1.0 / sqrt(-expm1((double)step * a.ln_beta2)));
+}
+
 template <bool EIGHT>
-__global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __restrict__ table, int64_t chunks,
-                                                        AdamwScalars a)
+__global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __restrict__ table, AdamwScalars a)
 {
     // a table of other states or of fewer chunks than the caller says is not run
     if (table->magic != ADAMW_MAGIC || table->bits != (EIGHT ? 8 : 32) || (int64_t)blockIdx.x >= table->chunks) return;
@@ -156,21 +173,24 @@ __global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __rest
     const AdamwChunk* map = reinterpret_cast<const AdamwChunk*>(entries + table->count);
     const AdamwChunk ck = map[blockIdx.x];
     const AdamwEntry t = entries[ck.tensor];
-    const int64_t i0 = (int64_t)ck.index * adw::CHUNK + threadIdx.x * 8;
 
-    int64_t step = a.step_dev ? *a.step_dev : a.step;
-    step = step < 1 ? 1 : step;
+    int64_t step = a.step;
     const float lr = a.lr_dev ? *a.lr_dev : a.lr;
     const float gs = a.grad_scale_dev ? *a.grad_scale_dev : 1.0f;
-    const float ibc1 = (float)(-1.0 / expm1((double)step * a.ln_beta1));
-    const float rsbc2 = (float)(1.0 / sqrt(-expm1((double)step * a.ln_beta2)));
+    float ibc1 = a.ibc1, rsbc2 = a.rsbc2;
+    if (a.step_dev) {
+        step = *a.step_dev;
+        step = step < 1 ? 1 : step;
+        bias_corrections(a, step, ibc1, rsbc2);
+    }
     const float decay = 1.0f - lr * t.weight_decay;
     const float lrm = lr * ibc1;
 
+    const int64_t i0 = (int64_t)ck.index * adw::CHUNK + threadIdx.x * 8;
     // lanes past the tensor's end take no part in its loads and stores, but their quad's amax may
     // need them as zeros: a quad is left only as a whole
+    if ((i0 & ~(int64_t)31) >= t.n) return;
     const int64_t left = t.n - i0;
-    if (((i0 & ~(int64_t)31)) >= t.n) return;
     const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
 
     float p[8], g[8], m[8], v[8];
@@ -205,12 +225,15 @@ __global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __rest
         if (t.copy) store_bf16(static_cast<uint16_t*>(t.copy) + i0, n, p);
     }
     if constexpr (EIGHT) {
-        const uint64_t seed = a.seed + (uint64_t)step;
+        const uint64_t seed = a.seed + (uint64_t)step, blk = (uint64_t)i0 >> 3;
         const uint32_t stream = a.rng_stream + 2u * (uint32_t)ck.tensor;
-        store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.m_e8m0 + (i0 >> 5), n, m, seed, stream,
-                           (uint64_t)i0 >> 3);
-        store_codes<true>(static_cast<uint8_t*>(t.v) + i0, t.v_e8m0 + (i0 >> 5), n, root, seed, stream + 1u,
-                          (uint64_t)i0 >> 3);
+        const int em = block_exponent(m), ev = block_exponent(root);
+        // 2^-e of both, one powf a lane: even lanes of a quad take m's, odd ones v's
+        const float inv = powf(2.0f, (float)-(threadIdx.x & 1 ? ev : em));
+        store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.m_e8m0 + (i0 >> 5), n, m, em, quad_lane<0>(inv), seed,
+                           stream, blk);
+        store_codes<true>(static_cast<uint8_t*>(t.v) + i0, t.v_e8m0 + (i0 >> 5), n, root, ev, quad_lane<1>(inv), seed,
+                          stream + 1u, blk);
     } else if (n > 0) {
         store_f32(static_cast<float*>(t.m) + i0, n, m);
         store_f32(static_cast<float*>(t.v) + i0, n, v);
@@ -221,9 +244,9 @@ hipError_t launch_adamw(const void* table, int64_t chunks, int bits, const Adamw
 {
     const AdamwTable* t = static_cast<const AdamwTable*>(table);
     if (bits == 8)
-        hipLaunchKernelGGL((k_adamw<true>), dim3((unsigned)chunks), dim3(adw::THREADS), 0, stream, t, chunks, a);
+        hipLaunchKernelGGL((k_adamw<true>), dim3((unsigned)chunks), dim3(adw::THREADS), 0, stream, t, a);
     else
-        hipLaunchKernelGGL((k_adamw<false>), dim3((unsigned)chunks), dim3(adw::THREADS), 0, stream, t, chunks, a);
+        hipLaunchKernelGGL((k_adamw<false>), dim3((unsigned)chunks), dim3(adw::THREADS), 0, stream, t, a);
     return hipGetLastError();
 }
 

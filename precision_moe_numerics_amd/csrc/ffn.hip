@@ -12,11 +12,8 @@
 // dgrad, both operands in wgrad).
 //
 // Operands stream through a ring of LDS stages of 32 k, filled by buffer_load ... lds (global -> LDS
-// without registers), 1 KB pieces dealt evenly to the wavefronts. Two stages are filled together, a
-// piece's two halves one after the other: a row of a k-contiguous operand gives 64 bytes to a stage,
-// and the second half of the 128-byte line then comes from the first-level cache instead of a second
-// time from L2. "The pair has landed" is the per-wavefront condition vmcnt <= loads issued after it,
-// followed by a barrier. A wavefront reads the fragments of stage v + 1 while the MFMAs of stage v run
+// without registers), 1 KB pieces dealt evenly to the wavefronts, so "stage s has landed" is the
+// per-wavefront condition vmcnt <= loads issued after it, followed by a barrier. A wavefront reads the fragments of stage v + 1 while the MFMAs of stage v run
 // from registers. Bounds are the buffer descriptor's: rows and k past the operand read as zeros, so
 // every size that is a multiple of 8 runs the same code.
 //   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
@@ -149,7 +146,7 @@ PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
 
 constexpr uint32_t FFN_OUTSIDE = 0x80000000u;   // a buffer offset past every descriptor
 
-// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages
+// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of 5 filled in pairs
 template <int WR_, int WC_, int RB_, int CB_, int NST_>
 struct FfnTile {
     static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
@@ -159,10 +156,11 @@ struct FfnTile {
     static constexpr int RPW = BR / 16 / (WR * WC), CPW = BC / 16 / (WR * WC), PPW = RPW + CPW;   // pieces per wavefront
     static constexpr int OPITCH = BR + 4;                       // floats per staged output row
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
-    static constexpr int RING = NST * STAGE, OUTB = OROWS * OPITCH * 4;
+    static constexpr bool PAIRS = RPW % 2 == 0 && CPW % 2 == 0;
+    static constexpr int RING = (PAIRS ? 5 : NST) * STAGE, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
-    static_assert((NST - 1) * PPW <= 63, "vmcnt");
+    static_assert((PAIRS ? 6 : NST - 1) * PPW <= 63, "vmcnt");
 };
 
 // Tile i of a product's rtiles x ctiles for workgroup L: workgroups L, L + 8, .. run on one XCD and take
@@ -184,8 +182,9 @@ PMN_DEV bool ffn_tile_of(const FfnArgs& p, int64_t L, int64_t& trow, int64_t& tc
 template <typename T, bool RKC, bool CKC, int EPI>
 PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, uint8_t* lds)
 {
-    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, NST = T::NST, PPW = T::PPW;
-    constexpr bool SWI = EPI == FFN_SWIGLU;
+    constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, PPW = T::PPW;
+    constexpr bool SWI = EPI == FFN_SWIGLU, PAIRED = T::PAIRS && RKC && CKC;
+    constexpr int NST = PAIRED ? 5 : T::NST;
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -313,15 +312,12 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // One step: stage v + 1 has landed and every wavefront is done reading stage v, whose slot is
-    // refilled with stage v + NST. The loads are spread over the step's MFMAs and the fragment reads over
-    // the first three quarters of them, so that the last have come back before the next step's barrier
-    // (all loads before all reads measured 4% slower, loads of two stages at a time 15%).
+    // The MFMAs of a step with its PPW loads spread over them and the fragment reads of stage `next`
+    // over the first three quarters, so that the last have come back before the next step's barrier
+    // (all loads before all reads measured 4% slower).
     constexpr int NM = 2 * RB * CB, NRQ = NM * 3 / 4;
-    auto step = [&](int v, const Frags& cur, Frags& nxt) {
-        wait_loads_and_barrier<(NST - 2) * PPW>();
-        const Stage g = stage_at(v + NST);
-        const uint8_t* rbase = lds + ((v + 1) % NST) * T::STAGE;
+    auto compute = [&](int next, const Frags& cur, Frags& nxt, auto load) {
+        const uint8_t* rbase = lds + (next % NST) * T::STAGE;
 #pragma unroll
         for (int q = 0; q < NM; q++) {
             const int ks = q / (RB * CB), i = (q / CB) % RB, j = q % CB;
@@ -329,27 +325,67 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 #pragma unroll
             for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
 #pragma unroll
-            for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) issue_piece(g, n);
+            for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) load(n);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    {
+    Frags f0, f1;
+    auto read_first = [&] {
+#pragma unroll
+        for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
+    };
+    if constexpr (!PAIRED) {
 #pragma unroll
         for (int s = 0; s < NST; s++) {
             const Stage g = stage_at(s);
 #pragma unroll
             for (int i = 0; i < PPW; i++) issue_piece(g, i);
         }
-        Frags f0, f1;
         wait_loads_and_barrier<(NST - 1) * PPW>();
-#pragma unroll
-        for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
+        read_first();
+        // stage v + 1 has landed and every wavefront is done reading stage v, whose slot is refilled
+        auto step = [&](int v, const Frags& cur, Frags& nxt) {
+            wait_loads_and_barrier<(NST - 2) * PPW>();
+            const Stage g = stage_at(v + NST);
+            compute(v + 1, cur, nxt, [&](int n) { issue_piece(g, n); });
+        };
         for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
             step(v, f0, f1);
             step(v + 1, f1, f0);
         }
-        wait_loads_and_barrier<0>();
+    } else {
+        // Both operands k-contiguous: a row gives 64 bytes to a stage, half a 128-byte line. Stages go in
+        // pairs v, v + 1 (v even): a piece is loaded for both stages back to back, so that the second half
+        // of its lines is in the first-level cache (8192 x 7168 x 2048 forward: 707 us with single stages,
+        // 660 in pairs; row-contiguous operands, whose stages are whole lines, lose 5% by it). Slots of
+        // stages v - 1 and v are free at step v; half of the pieces are loaded then, half at step v + 1.
+#pragma unroll
+        for (int s = 0; s < NST - 1; s += 2) {
+            const Stage g0 = stage_at(s), g1 = stage_at(s + 1);
+#pragma unroll
+            for (int i = 0; i < PPW; i++) {
+                issue_piece(g0, i);
+                issue_piece(g1, i);
+            }
+        }
+        wait_loads_and_barrier<(NST - 3) * PPW>();
+        read_first();
+        auto step = [&](int v, int odd, const Frags& cur, Frags& nxt) {
+            const Stage g0 = stage_at(v + NST - 1), g1 = stage_at(v + NST);
+            compute(v + odd + 1, cur, nxt, [&](int n) {
+                const bool isr = n < T::RPW;
+                const int m = isr ? n : n - T::RPW, half = (isr ? T::RPW : T::CPW) / 2;
+                issue_piece(m & 1 ? g1 : g0, (isr ? 0 : T::RPW) + odd * half + (m >> 1));
+            });
+        };
+        for (int v = 0; v < nst; v += 2) {
+            wait_loads_and_barrier<63>();      // stage v + 1 landed with its pair
+            step(v, 0, f0, f1);
+            wait_loads_and_barrier<PPW>();     // the pair v + 2, v + 3: all but step v's loads
+            step(v, 1, f1, f0);
+        }
     }
+    wait_loads_and_barrier<0>();
 
     // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]; a thread finishes NP pieces
     // of 8 values, whose words of aux are on their way while the rows are staged

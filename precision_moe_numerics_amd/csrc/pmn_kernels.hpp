@@ -186,6 +186,7 @@ struct AdamwChunk {
 };
 struct AdamwScalars {
     float lr, beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
+    float ibc1, rsbc2;               // 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
     double ln_beta1, ln_beta2;
     int64_t step;
     const float* lr_dev;             // nullable: read instead of lr, step
