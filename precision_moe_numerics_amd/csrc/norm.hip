@@ -12,15 +12,16 @@
 // Both are bound by HBM traffic: every value is read once into registers (a row is held by one
 // wavefront, 512 or 1024 threads, in 16-byte pieces of 8 values) and written once: 16384 rows of 4096
 // with a bf16 residual move 606 MB forward (y and codes out) in 107 us, 537 MB backward in 107 us, 5.7
-// and 5.0 TB/s where a copy of 1 GB reaches 5.1. Sums are fp32:
-// a thread's values in order, then a butterfly over the lanes, then the wavefronts in order, so
-// results do not depend on the launch.
+// and 5.0 TB/s where a copy of 1 GB reaches 5.1. Sums (fp64
+// forward, fp32 backward) take a thread's values in order, then a butterfly over the lanes, then the
+// wavefronts in order, so results do not depend on the launch.
 #include "pmn_dev.hpp"
 #include "pmn_kernels.hpp"
 
 namespace pmn {
 
-PMN_DEV float wave_sum(float v)
+template <typename S>
+PMN_DEV S wave_sum(S v)
 {
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
@@ -62,16 +63,16 @@ PMN_DEV void store8(float* p, const float (&v)[8])
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Sum over the T threads of a row. red: T / 64 floats (two sets used in turn by a loop over rows,
+// Sum over the T threads of a row. red: T / 64 values (two sets used in turn by a loop over rows,
 // so one barrier per row is enough). T = 64: the wavefront alone.
-template <int T>
-PMN_DEV float row_sum(float v, float* red)
+template <int T, typename S>
+PMN_DEV S row_sum(S v, S* red)
 {
     v = wave_sum(v);
     if (T == 64) return v;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    float s = 0.0f;
+    S s = 0;
 #pragma unroll
     for (int w = 0; w < T / 64; w++) s += red[w];
     return s;
@@ -86,13 +87,15 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
 {
     constexpr bool HAS_RES = !__is_same(R, uint8_t);
     constexpr int RPB = T < 256 ? 256 / T : 1;
-    __shared__ float red[T / 64];
+    __shared__ double red[T / 64];
     const int t = threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
     if (row >= rows) return;   // whole wavefronts (T >= 64); with T > 64 the whole workgroup
     const int nch = C >> 3;
+    // The squares are summed in fp64: an error of s moves a whole row's y, and with it every E4M3 code of
+    // the row that lies next to a tie. The kernel stays bound by its traffic.
     float z[CH][8];
-    float ss = 0.0f;
+    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const int c = t + i * T;
@@ -106,11 +109,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
                 store8(z_out + row * C + 8 * c, z[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; j++) ss = __builtin_fmaf(z[i][j], z[i][j], ss);
+            for (int j = 0; j < 8; j++) ss = __builtin_fma((double)z[i][j], (double)z[i][j], ss);
         }
     }
     ss = row_sum<T>(ss, red);
-    const float s = 1.0f / sqrtf(ss / (float)C + eps);
+    const float s = (float)(1.0 / sqrt(ss / (double)C + (double)eps));
     if (rstd && t == 0) rstd[row] = s;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
