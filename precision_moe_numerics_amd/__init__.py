@@ -835,40 +835,47 @@ class AdamWPlan:
         dev = self.tensors[0].param.device
         self.state_bits = 8 if self.tensors[0].m.dtype == torch.uint8 else 32
         sdt = torch.uint8 if self.state_bits == 8 else torch.float32
+        at = dev.index if dev.type == "cuda" else -1
+        entries = (_AdamWEntry * len(self.tensors))()
         spans = []
         for i, t in enumerate(self.tensors):
             n = t.param.numel()
-            name = f"tensors[{i}]"
-            _need(t.param.dtype == torch.float32, f"{name}.param must be fp32")
-            _dtype_code(t.grad, f"{name}.grad")
-            for what, v, dt, k in (("grad", t.grad, t.grad.dtype, n), ("m", t.m, sdt, n), ("v", t.v, sdt, n),
-                                   ("copy", t.copy, torch.bfloat16, n), ("m_e8m0", t.m_e8m0, torch.uint8, (n + 31) // 32),
-                                   ("v_e8m0", t.v_e8m0, torch.uint8, (n + 31) // 32)):
-                if what in ("m_e8m0", "v_e8m0") and self.state_bits == 32:
-                    _need(v is None, f"{name}.{what} belongs to states in 8 bits")
-                elif what != "copy" or v is not None:
-                    _need(v is not None and v.dtype == dt and v.numel() == k, f"{name}.{what} must hold {k} values of {dt}")
-            for what in ("param", "grad", "m", "v", "copy", "m_e8m0", "v_e8m0"):
+            nb = (n + 31) // 32
+            ptr = {}
+            for what, dt, k in (("param", torch.float32, n), ("grad", None, n), ("m", sdt, n), ("v", sdt, n),
+                                ("copy", torch.bfloat16, n), ("m_e8m0", torch.uint8, nb), ("v_e8m0", torch.uint8, nb)):
                 v = getattr(t, what)
-                if v is not None:
-                    _need(v.device == dev, f"{name}.{what} must be on {dev}")
-                    _need(v.is_contiguous(), f"{name}.{what} must be contiguous")
-                    if v.numel():
-                        spans.append((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size(), what != "grad", f"{name}.{what}"))
+                if what in ("m_e8m0", "v_e8m0") and self.state_bits == 32:
+                    _need(v is None, f"tensors[{i}].{what} belongs to states in 8 bits")
+                    continue
+                if what == "copy" and v is None:
+                    continue
+                if what == "grad":
+                    gcode = _dtype_code(v, f"tensors[{i}].grad")
+                    dt = v.dtype
+                if v is None or v.dtype != dt or v.numel() != k:
+                    raise PmnError(f"tensors[{i}].{what} must hold {k} values of {dt}")
+                if v.get_device() != at:
+                    raise PmnError(f"tensors[{i}].{what} must be on {dev}")
+                if not v.is_contiguous():
+                    raise PmnError(f"tensors[{i}].{what} must be contiguous")
+                p = ptr[what] = v.data_ptr()
+                if k:
+                    spans.append((p, p + k * v.element_size(), what != "grad", i, what))
+            entries[i] = _AdamWEntry(ptr["param"], ptr["grad"], ptr.get("copy"), ptr["m"], ptr["v"], ptr.get("m_e8m0"),
+                                     ptr.get("v_e8m0"), n, t.weight_decay, gcode)
         # buffers that are written overlap no other; gradients may share memory among themselves
         spans.sort()
-        end, owner, wend, wowner = 0, "", 0, ""
-        for lo, hi, written, name in spans:
-            _need(lo >= (end if written else wend), f"{name} overlaps {owner if written else wowner}")
+        end, owner, wend, wowner = 0, None, 0, None
+        for lo, hi, written, i, what in spans:
+            if lo < (end if written else wend):
+                j, other = owner if written else wowner
+                raise PmnError(f"tensors[{i}].{what} overlaps tensors[{j}].{other}")
             if hi > end:
-                end, owner = hi, name
+                end, owner = hi, (i, what)
             if written and hi > wend:
-                wend, wowner = hi, name
-        entries = (_AdamWEntry * len(self.tensors))()
-        for i, t in enumerate(self.tensors):
-            entries[i] = _AdamWEntry(_ptr(t.param), _ptr(t.grad), _ptr(t.copy), _ptr(t.m), _ptr(t.v), _ptr(t.m_e8m0),
-                                     _ptr(t.v_e8m0), t.param.numel(), t.weight_decay,
-                                     _dtype_code(t.grad, f"tensors[{i}].grad"))
+                wend, wowner = hi, (i, what)
+        _need(at >= 0, "the tensors must be on the GPU")
         size = _lib.adamw_table_size(entries, len(entries))
         host = torch.empty(((size + 7) // 8,), dtype=torch.int64)
         chunks = C.c_int64(0)
