@@ -499,7 +499,8 @@ int rmsnorm_residual_bwd(const void* dy, int dy_dtype, const void* z, int z_dtyp
  * bf16 [M x H] (the routed experts' sum; it may be y itself); h13_out: NULL, or bf16 [M x 2F], h1 | h3
  * for the backward; y bf16 [M x H]. a is rounded to bf16 for the second product.
  * H % 8 == 0, F % 8 == 0, H and F <= 2^20, 0 <= M <= 2^22 (PMN_ESHAPE); pointers 16-byte aligned (PMN_EALIGN). Workspace
- * (16-byte aligned, at least swiglu_ffn_fwd_workspace_size() bytes, PMN_EWORKSPACE).
+ * (16-byte aligned, at least swiglu_ffn_fwd_workspace_size() bytes, PMN_EWORKSPACE; no initialization;
+ * calls that overlap in time must not share one, here and below).
  */
 size_t swiglu_ffn_fwd_workspace_size(int64_t M, int64_t H, int64_t F);
 int swiglu_ffn_fwd(const void* x, const void* w13, const void* w2, const void* add, int64_t M, int64_t H,

@@ -13,9 +13,10 @@
 //
 // Operands stream through a ring of LDS stages of 32 k, filled by buffer_load ... lds (global -> LDS
 // without registers), 1 KB pieces dealt evenly to the wavefronts, so "stage s has landed" is the
-// per-wavefront condition vmcnt <= loads issued after it, followed by a barrier. A wavefront reads the fragments of stage v + 1 while the MFMAs of stage v run
-// from registers. Bounds are the buffer descriptor's: rows and k past the operand read as zeros, so
-// every size that is a multiple of 8 runs the same code.
+// per-wavefront condition vmcnt <= loads issued after it, followed by a barrier. A wavefront reads the
+// fragments of stage v + 1 while the MFMAs of stage v run from registers. Bounds are the buffer
+// descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
+// the same code.
 //   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
 //     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured).
 //   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
@@ -37,7 +38,6 @@ namespace pmn {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 enum { FFN_SWIGLU = 0, FFN_ADD = 1, FFN_SWIGLU_BWD = 2, FFN_BF16 = 3, FFN_F32 = 4, FFN_PART = 5 };
 
@@ -201,12 +201,20 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 
     // This wavefront's pieces, RPW of R and then CPW of C: byte offset of the lane's 16 bytes from the
     // operand's first at the stage, and for a k-contiguous operand the lane's first k of the stage.
+    // Workgroups that share a panel start at different pieces of it, or they would ask one L2 channel for
+    // the same lines at once: 4 to 5% at 128 x 128 (600 .. 2000 rows forward); 256 x 256 tiles are bound by
+    // their MFMAs and run 1% slower with it.
+    constexpr bool ROTATE = RB * CB < 16;
+    const int rotr = ROTATE ? (int)(tcol % (BR / 16)) : 0, rotc = ROTATE ? (int)(trow % (BC / 16)) : 0;
+    auto piece_of = [&](int i) {   // piece of its operand's tile
+        return i < T::RPW ? (wave * T::RPW + i + rotr) % (BR / 16) : (wave * T::CPW + i - T::RPW + rotc) % (BC / 16);
+    };
     uint32_t voff[PPW];
     int kch[PPW];
 #pragma unroll
     for (int i = 0; i < PPW; i++) {
         const bool isr = i < T::RPW;
-        const int q = isr ? wave * T::RPW + i : wave * T::CPW + i - T::RPW;
+        const int q = piece_of(i);
         const int64_t ld = isr ? p.ldr : p.ldc;
         if (isr ? RKC : CKC) {
             const int t = q * 16 + (lane >> 2);                       // tile row
@@ -233,7 +241,6 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
-    const uint32_t rdst = lds0 + wave * T::RPW * 1024, cdst = lds0 + T::RBYTES + wave * T::CPW * 1024;
     // An operand's bytes from its first at stage 0 of this part, a stage's advance and how many bytes
     // there are (a k-contiguous operand is bounded by rows and chunks instead)
     struct Operand {
@@ -271,15 +278,15 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         // chunks past K of a k-contiguous operand
         const uint32_t v = (isr ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i];
         if (!isr) {
-            dma16_buffer(g.c, v, g.dst + cdst + (i - T::RPW) * 1024);
+            dma16_buffer(g.c, v, g.dst + lds0 + T::RBYTES + piece_of(i) * 1024);
         } else if (!SWI) {
-            dma16_buffer(g.r, v, g.dst + rdst + i * 1024);
+            dma16_buffer(g.r, v, g.dst + lds0 + piece_of(i) * 1024);
         } else {
-            const bool w3 = ((wave * T::RPW + i) >> 1) % RB >= RB / 2;
+            const bool w3 = (piece_of(i) >> 1) % RB >= RB / 2;
             i32x4 d;
 #pragma unroll
             for (int q = 0; q < 4; q++) d[q] = __builtin_amdgcn_readfirstlane(w3 ? g.r3[q] : g.r[q]);
-            dma16_buffer(d, v, g.dst + rdst + i * 1024);
+            dma16_buffer(d, v, g.dst + lds0 + piece_of(i) * 1024);
         }
     };
 

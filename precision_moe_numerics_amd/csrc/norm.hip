@@ -81,8 +81,8 @@ PMN_DEV S row_sum(S v, S* red)
 // One row per T threads, CH pieces of 8 values each. R: the residual's type (void: none).
 template <int T, int CH, typename R>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
-    const uint16_t* __restrict__ x, const R* __restrict__ res, const float* __restrict__ gamma, float eps,
-    int64_t rows, int C, R* __restrict__ z_out, uint16_t* __restrict__ y, uint8_t* __restrict__ codes,
+    const uint16_t* __restrict__ x, const R* res, const float* __restrict__ gamma, float eps,
+    int64_t rows, int C, R* z_out, uint16_t* __restrict__ y, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ e8m0, float* __restrict__ rstd)
 {
     constexpr bool HAS_RES = !__is_same(R, uint8_t);
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
 template <int T, int CH, typename Z, typename D>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_bwd(
     const D* __restrict__ dy, const Z* __restrict__ zin, const float* __restrict__ gamma,
-    const float* __restrict__ rstd, const Z* __restrict__ dres, int64_t rows, int C, Z* __restrict__ dz,
+    const float* __restrict__ rstd, const Z* dres, int64_t rows, int C, Z* dz,
     float* __restrict__ part)
 {
     constexpr int RPB = T < 256 ? 256 / T : 1;

@@ -90,8 +90,9 @@ def exponent(amax):
     return np.where((e > -127) & (amax <= 448.0 * 2.0 ** (e - 1.0)), e - 1, e)
 
 
-def check_sr(codes, e8m0, value, seed, stream, positive, what):
-    """The stored codes are the stochastic rounding of `value` under (seed, stream)."""
+def check_sr(codes, e8m0, value, seed, stream, positive, what, first=0):
+    """The stored codes are the stochastic rounding of `value`, values `first` .. of a tensor, under
+    (seed, stream)."""
     n = value.numel()
     val = np.zeros((n + 31) // 32 * 32)
     val[:n] = value.numpy()
@@ -108,7 +109,7 @@ def check_sr(codes, e8m0, value, seed, stream, positive, what):
     step = 2.0 ** (np.floor(np.log2(np.maximum(y, 2.0 ** -6))) - 3)
     lo = np.floor(y / step) * step
     f = (y - lo) / step
-    r16 = O.rand16_array(seed, stream, np.arange(n)).astype(np.float64)
+    r16 = O.rand16_array(seed, stream, first + np.arange(n)).astype(np.float64)
     up = r16 < np.floor(f * 65536.0)
     expect = lo + step * up
     if positive:
@@ -256,3 +257,40 @@ def test_another_states_table_is_left_alone(P):
     assert all(torch.equal(a, b) for a, b in zip(before, (ts[0].param, ts[0].m, ts[0].v)))
     P.adamw_step(plan, lr=1e-2, step=1, **HY)   # chunks past the table's are skipped
     assert not torch.equal(before[0], ts[0].param) and torch.isfinite(ts[0].param).all()
+
+
+def test_empty_tensors_take_no_part(P):
+    """Tensors of no values beside others: the others' step is the one without them (each keeps its place
+    in the list, and with it its stream of random numbers)."""
+    for bits in (32, 8):
+        a, b = make(P, [100, 70], bits, torch.float32, 6), make(P, [100, 70], bits, torch.float32, 6)
+        none = P.AdamWTensor.new(torch.empty(0, device=DEV), torch.empty(0, device=DEV), bits)
+        P.adamw_step(P.AdamWPlan([a[0], a[1], none]), lr=1e-3, step=2, seed=4, **HY)
+        P.adamw_step(P.AdamWPlan(b), lr=1e-3, step=2, seed=4, **HY)
+        for s, t in zip(a, b):
+            assert torch.equal(s.param, t.param) and torch.equal(s.m, t.m) and torch.equal(s.v, t.v)
+        P.adamw_step(P.AdamWPlan([none]), lr=1e-3, step=2, **HY)
+
+
+def test_offsets_past_32_bits(P):
+    """A tensor of 2^31 + 5000 values (states in 8 bits, bf16 gradient): its last values against the same
+    values as a tensor of their own, with the random numbers of their indices through check_sr."""
+    n = (1 << 31) + 5000
+    p = torch.zeros(n, device=DEV)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    tail = 4096
+    gen = torch.Generator().manual_seed(3)
+    p[-tail:] = torch.randn(tail, generator=gen).to(DEV) * 0.02
+    g[-tail:] = (torch.randn(tail, generator=gen) * 1e-2).to(torch.bfloat16).to(DEV)
+    t = P.AdamWTensor.new(p, g, 8)
+    small = P.AdamWTensor.new(p[-tail:].clone(), g[-tail:].clone(), 32)
+    refs = reference(small, 32, 1e-2, 1)
+    P.adamw_step(P.AdamWPlan([t]), lr=1e-2, step=1, seed=3, **HY)
+    within(t.param[-tail:], refs[0], refs[1], "p")
+    assert (t.param[:1000] == 0).all() and (t.param[(1 << 31):(1 << 31) + 100] == 0).all()
+    # the last whole blocks: the tail begins inside one, 5000 - 4096 = 904 = 28 * 32 + 8
+    at = n - tail + 24
+    assert at % 32 == 0
+    m, v = refs[2][24:], refs[4][24:]
+    check_sr(t.m[at:], t.m_e8m0[at // 32:], m, 3 + 1, 0, False, "m", first=at)
+    check_sr(t.v[at:], t.v_e8m0[at // 32:], v.sqrt(), 3 + 1, 1, True, "v", first=at)

@@ -39,6 +39,7 @@ def D(c, k):
 
 
 def ref_fwd(c):
+    """On the device of c's tensors, in fp64."""
     F = c["w2"].shape[1]
     x, w13, w2 = D(c, "x"), D(c, "w13"), D(c, "w2")
     H = x.shape[1]
@@ -56,7 +57,7 @@ def ref_fwd(c):
 
 
 def within(got, ref, bound, what):
-    bad = ~((got.double().cpu() - ref).abs() <= bound)
+    bad = ~((got.to(ref.device).double() - ref).abs() <= bound)
     assert not bad.any(), f"{what}: {int(bad.sum())} values outside the bound, first at {bad.nonzero()[0].tolist()}"
 
 
@@ -244,3 +245,48 @@ def test_streams_and_graph(P, M):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, call())), f"replay {k}"
+
+
+# sizes that reach the 256 x 256 tiles (160 of them and more), ragged at every edge; fp64 on the GPU
+@pytest.mark.parametrize("M,H,F", [(2600, 264, 2056), (2600, 4104, 72), (1300, 2056, 1288)])
+def test_forward_of_many_tiles(P, M, H, F):
+    d = dev(case(M, H, F, M + H + F))
+    h, hb, y, yb = ref_fwd(d)
+    got, h13 = P.swiglu_ffn_fwd(d["x"], d["w13"], d["w2"], add=d["add"], save_h13=True)
+    within(h13, h, hb, "h13")
+    within(got, y, yb, "y")
+
+
+@pytest.mark.parametrize("M,H,F", [(5000, 2600, 2056), (5000, 5000, 1032), (3000, 264, 136), (9000, 72, 264)])
+def test_backward_of_many_tiles(P, M, H, F):
+    d = dev(bwd_case(M, H, F, M + H + F))
+    ref = ref_bwd(d)
+    for dt, half in ((torch.float32, 0.0), (torch.bfloat16, B)):
+        got = dict(zip(("dx", "dw13", "dw2"), P.swiglu_ffn_bwd(d["dy"], d["x"], d["w13"], d["w2"], d["h13"], dw_dtype=dt)))
+        for k, (r, e) in ref.items():
+            within(got[k], r, e + ((B if k == "dx" else half) + U) * (r.abs() + e), f"{k} {dt}")
+
+
+def test_offsets_past_32_bits(P):
+    """300000 rows of 7168 (2.15 G values, 4.3 GB): the last rows against fp64, the rows just past 2^31
+    values too, and the weights' gradients of a dy that is zero but in those rows."""
+    M, H, F = 300_000, 7168, 32
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty((M, H), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    c = case(8, H, F, 3, add=False)
+    d = dict(w13=c["w13"].to(DEV), w2=c["w2"].to(DEV))
+    y, h13 = P.swiglu_ffn_fwd(x, d["w13"], d["w2"], save_h13=True)
+    rows = torch.cat([torch.arange(299_590, 299_600), torch.arange(M - 40, M)]).to(DEV)
+    part = dict(d, x=x[rows].clone(), add=None)
+    h, hb, yr, yb = ref_fwd(part)
+    within(h13[rows], h, hb, "h13")
+    within(y[rows], yr, yb, "y")
+    dy = y.zero_()
+    dy[rows] = torch.empty((50, H), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    dx, dw13, dw2 = P.swiglu_ffn_bwd(dy, x, d["w13"], d["w2"], h13)
+    ref = ref_bwd(dict(part, dy=dy[rows].clone(), h13=h13[rows].clone()))
+    within(dx[rows], ref["dx"][0], ref["dx"][1] + (B + U) * (ref["dx"][0].abs() + ref["dx"][1]), "dx")
+    assert (dx[:1000] == 0).all()
+    # M terms in the sums, all but 50 of them zero: exact
+    for k, got in (("dw13", dw13), ("dw2", dw2)):
+        within(got, ref[k][0], ref[k][1] + U * ref[k][0].abs(), k)

@@ -52,7 +52,7 @@ def gpu(*ts):
 
 
 def within(got, ref, bound, what):
-    bad = (got.double().cpu() - ref).abs() > bound
+    bad = (got.to(ref.device).double() - ref).abs() > bound
     assert not bad.any(), f"{what}: {int(bad.sum())} values outside the bound, first at {bad.nonzero()[0].tolist()}"
 
 
@@ -231,3 +231,22 @@ def test_streams_and_graph(P):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, call())), f"replay {k}"
+
+
+def test_offsets_past_32_bits(P):
+    """300000 rows of 7168 (2.15 G values): the rows just past 2^31 values and the last ones."""
+    M, C = 300_000, 7168
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.empty((M, C), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    r = torch.empty((M, C), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    gamma = torch.ones(C, device=DEV)
+    o = P.rmsnorm_residual_fwd(x, gamma, residual=r, want_mxfp8=True, want_rstd=True)
+    rows = torch.cat([torch.arange(299_590, 299_600), torch.arange(M - 10, M)]).to(DEV)
+    few = P.rmsnorm_residual_fwd(x[rows].contiguous(), gamma, residual=r[rows].contiguous(), want_mxfp8=True, want_rstd=True)
+    for k in ("y", "z", "codes", "e8m0", "rstd"):
+        assert torch.equal(getattr(o, k)[rows], getattr(few, k)), k
+    del x, r
+    z = o.z[rows].contiguous()
+    dz, _ = P.rmsnorm_residual_bwd(o.y, o.z, gamma, o.rstd)
+    again, _ = P.rmsnorm_residual_bwd(few.y, z, gamma, few.rstd)
+    assert torch.equal(dz[rows], again)
