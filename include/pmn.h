@@ -463,13 +463,13 @@ int pmn_check_indices(const int64_t* offsets, int G, int64_t M, const int32_t* g
 
 /*
  * Root-mean-square norm of x bf16 [rows x cols] with the residual's addition:
- *   z = x + residual (fp32), s = 1 / sqrt(mean(z^2) + eps) per row, y = z s gamma.
+ *   z = x + residual, s = 1 / sqrt(mean(z^2) + eps) per row, y = z s gamma.
  * residual: NULL (z = x; z_out is not used), or [rows x cols] of res_dtype (PMN_DTYPE_*), and then
- *   z_out, of the same type, receives z (it may be residual itself). y is computed from the fp32 z.
+ *   z_out, of the same type, receives z (it may be residual itself). y is computed from z itself.
  * gamma: fp32 [cols]. Outputs, each nullable but at least one of y and codes given: y bf16
  *   [rows x cols]; codes uint8 [rows x cols] and e8m0 uint8 [rows x cols/32], the row-wise MXFP8 form
- *   of the fp32 y (scale rule and rounding to nearest even as mxfp8_quantize; a NaN or infinite y
- *   has a NaN code, 0x7F or 0xFF); rstd fp32 [rows], s for the backward.
+ *   of y before any rounding to bf16 (scale rule and rounding to nearest even as mxfp8_quantize; a NaN
+ *   or infinite y has a NaN code, 0x7F or 0xFF); rstd fp32 [rows], s for the backward.
  * cols % 8 == 0 (with codes: cols % 32 == 0), cols <= 32768, rows < 2^31 (PMN_ESHAPE); eps >= 0
  * (PMN_EINVAL); every pointer 16-byte aligned but e8m0 (any) and rstd (4) (PMN_EALIGN).
  */

@@ -3,18 +3,18 @@
 //
 // Forward, per row of C values:
 //     z = x + r,   s = 1 / sqrt(mean(z^2) + eps),   y = z s gamma
-// z (the residual stream after the addition) is written in r's type; the norm uses the fp32 sum
-// itself, so y is rounded once. MXFP8 codes take y in fp32 (not the bf16 output): e is the smallest
-// exponent with max|y| <= 448 * 2^e over 32 values, code = E4M3(y 2^-e) to nearest even.
+// z (the residual stream after the addition) is written in r's type; the norm uses the sum itself, so
+// y is rounded once. MXFP8 codes take y itself, not the bf16 output: e is the smallest exponent with
+// max|y| <= 448 * 2^e over 32 values, code = E4M3(y 2^-e) to nearest even.
 // Backward, with xh = z s and t = dy gamma:
 //     dz = s (t - xh mean(t xh)) + dres,   dgamma = sum over rows of dy xh
 //
 // Both are bound by HBM traffic: every value is read once into registers (a row is held by one
 // wavefront, 512 or 1024 threads, in 16-byte pieces of 8 values) and written once: 16384 rows of 4096
 // with a bf16 residual move 606 MB forward (y and codes out) in 107 us, 537 MB backward in 107 us, 5.7
-// and 5.0 TB/s where a copy of 1 GB reaches 5.1. Sums (fp64
-// forward, fp32 backward) take a thread's values in order, then a butterfly over the lanes, then the
-// wavefronts in order, so results do not depend on the launch.
+// and 5.0 TB/s where a copy of 1 GB reaches 5.1. Sums (fp64 forward, fp32 backward) take a thread's
+// values in order, then a butterfly over the lanes, then the wavefronts in order, so results do not
+// depend on the launch.
 #include "pmn_dev.hpp"
 #include "pmn_kernels.hpp"
 
@@ -78,7 +78,7 @@ PMN_DEV S row_sum(S v, S* red)
     return s;
 }
 
-// One row per T threads, CH pieces of 8 values each. R: the residual's type (void: none).
+// One row per T threads, CH pieces of 8 values each. R: the residual's type (uint8_t: none).
 template <int T, int CH, typename R>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
     const uint16_t* __restrict__ x, const R* res, const float* __restrict__ gamma, float eps,
@@ -92,8 +92,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
     if (row >= rows) return;   // whole wavefronts (T >= 64); with T > 64 the whole workgroup
     const int nch = C >> 3;
-    // The squares are summed in fp64: an error of s moves a whole row's y, and with it every E4M3 code of
-    // the row that lies next to a tie. The kernel stays bound by its traffic.
+    // An error of y turns the E4M3 codes that lie next to a tie: the squares are summed in fp64, and the
+    // errors of s and of the products (from fma) are put back before the codes. (y in fp64, or with z's
+    // own rounding and the last one put back too, turned no code and was 4 to 10% slower.)
     float z[CH][8];
     double ss = 0.0;
 #pragma unroll
@@ -113,7 +114,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
         }
     }
     ss = row_sum<T>(ss, red);
-    const float s = (float)(1.0 / sqrt(ss / (double)C + (double)eps));
+    const double sd = 1.0 / sqrt(ss / (double)C + (double)eps);
+    const float s = (float)sd, sl = (float)(sd - (double)s);
     if (rstd && t == 0) rstd[row] = s;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
@@ -122,7 +124,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rmsnorm_fwd(
             float g[8];
             load8(gamma + 8 * c, g);
 #pragma unroll
-            for (int j = 0; j < 8; j++) z[i][j] = z[i][j] * s * g[j];
+            for (int j = 0; j < 8; j++) {
+                const float v = z[i][j], p = v * s, e = __builtin_fmaf(v, sl, __builtin_fmaf(v, s, -p));
+                z[i][j] = __builtin_fmaf(p, g[j], e * g[j]);
+            }
             if (y) store8(y + row * C + 8 * c, z[i]);
             if (codes) {
                 float amax = 0.0f;
