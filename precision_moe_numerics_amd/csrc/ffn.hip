@@ -547,7 +547,7 @@ __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
 // through LDS: one launch, no workspace. Columns past Nc repeat the last row and are not stored. Each
 // workgroup reads all of C from L2, so beyond 16 rows the ring's tiles with a split contraction are
 // faster (32 rows of 7168 x 2048: 35 us, this kernel with two column tiles 42).
-// One row of 7168 x 2048 (88 MB of weights): 12 us and 8 us, 4.9 and 3.7 TB/s.
+// One row of 7168 x 2048 (88 MB of weights): 12.6 us and 6.9 us, 4.7 and 4.3 TB/s.
 template <int EPI>
 __global__ __launch_bounds__(512, 2) void k_ffn_few(FfnArgs p)
 {
