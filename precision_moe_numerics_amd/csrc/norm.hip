@@ -282,12 +282,15 @@ template <typename R>
 static void rmsnorm_fwd_typed(const uint16_t* x, const R* res, const float* gamma, float eps, int64_t rows, int64_t C,
                               R* z, uint16_t* y, uint8_t* codes, uint8_t* e8m0, float* rstd, hipStream_t stream)
 {
+    // a launch holds fewer than 2^32 threads: at most 2^31 / T rows in one
 #define PMN_CALL(T, CH)                                                                                            \
-    {                                                                                                              \
+    for (int64_t r0 = 0; r0 < rows; r0 += ((int64_t)1 << 31) / (T)) {                                              \
+        const int64_t most = ((int64_t)1 << 31) / (T), n = rows - r0 < most ? rows - r0 : most, o = r0 * C;        \
         const int rpb = (T) < 256 ? 256 / (T) : 1;                                                                 \
-        hipLaunchKernelGGL((k_rmsnorm_fwd<T, CH, R>), dim3((unsigned)((rows + rpb - 1) / rpb)),                    \
-                           dim3((T) < 256 ? 256 : (T)), 0, stream, x, res, gamma, eps, rows, (int)C, z, y, codes,  \
-                           e8m0, rstd);                                                                            \
+        hipLaunchKernelGGL((k_rmsnorm_fwd<T, CH, R>), dim3((unsigned)((n + rpb - 1) / rpb)),                       \
+                           dim3((T) < 256 ? 256 : (T)), 0, stream, x + o, res ? res + o : nullptr, gamma, eps, n,  \
+                           (int)C, z ? z + o : nullptr, y ? y + o : nullptr, codes ? codes + o : nullptr,          \
+                           e8m0 ? e8m0 + o / 32 : nullptr, rstd ? rstd + r0 : nullptr);                            \
     }
     PMN_NORM_DISPATCH(C);
 #undef PMN_CALL

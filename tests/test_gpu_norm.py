@@ -250,3 +250,17 @@ def test_offsets_past_32_bits(P):
     dz, _ = P.rmsnorm_residual_bwd(o.y, o.z, gamma, o.rstd)
     again, _ = P.rmsnorm_residual_bwd(few.y, z, gamma, few.rstd)
     assert torch.equal(dz[rows], again)
+
+
+def test_more_rows_than_a_launch_holds(P):
+    """2^26 + 5 rows of 8 values are more than 2^32 threads in all: rows at the ends, around the border
+    of two launches (2^25) and a random choice against the same rows alone."""
+    M, C = (1 << 26) + 5, 8
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty((M, C), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    gamma = torch.linspace(0.5, 1.5, C, device=DEV)
+    o = P.rmsnorm_residual_fwd(x, gamma, want_rstd=True)
+    rows = torch.cat([torch.arange(8), torch.arange((1 << 25) - 8, (1 << 25) + 8), torch.arange(M - 16, M),
+                      torch.randint(0, M, (100_000,), generator=torch.Generator().manual_seed(4))]).to(DEV)
+    few = P.rmsnorm_residual_fwd(x[rows].contiguous(), gamma, want_rstd=True)
+    assert torch.equal(o.y[rows], few.y) and torch.equal(o.rstd[rows], few.rstd)
