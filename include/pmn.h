@@ -552,7 +552,8 @@ typedef struct {
  * the table into `table` (host memory, adamw_table_size bytes, 8-byte aligned) and its chunk count into
  * *chunks (host). The caller copies the table to the device and keeps it there for as many steps
  * as the pointers in it stay valid. Device pointers 16-byte aligned, e8m0 any (PMN_EALIGN). A tensor
- * may not appear twice: the calls read and write every buffer once, in no order.
+ * may not appear twice: the calls read and write every buffer once, in no order. A chunk holds up to
+ * 2048 values of one tensor; a table has fewer than 2^24 of them (PMN_ESHAPE).
  */
 size_t adamw_table_size(const pmn_adamw_tensor* tensors, int count);
 int adamw_table_build(const pmn_adamw_tensor* tensors, int count, int state_bits, void* table, size_t bytes,

@@ -574,6 +574,8 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
         wgrad ? dw13 : nullptr, dw2, dw_dtype == PMN_DTYPE_F32, hs(stream)));
 }
 
+// a chunk has 256 threads, and a launch fewer than 2^32
+constexpr int64_t ADAMW_MOST_CHUNKS = (int64_t)1 << 24;
 static int64_t adamw_chunks_of(int64_t n) { return n <= 0 ? 0 : (n + pmn::adamw_chunk() - 1) / pmn::adamw_chunk(); }
 
 size_t adamw_table_size(const pmn_adamw_tensor* tensors, int count)
@@ -602,7 +604,7 @@ int adamw_table_build(const pmn_adamw_tensor* tensors, int count, int state_bits
             return PMN_EALIGN;
         total += adamw_chunks_of(t.n);
     }
-    if (total >= ((int64_t)1 << 31)) return PMN_ESHAPE;
+    if (total >= ADAMW_MOST_CHUNKS) return PMN_ESHAPE;
     if (!table || bytes < adamw_table_size(tensors, count)) return PMN_EWORKSPACE;
     if (!aligned(table, 8)) return PMN_EALIGN;
     pmn::AdamwTable* head = static_cast<pmn::AdamwTable*>(table);
@@ -626,7 +628,7 @@ int adamw_step(const void* table, int64_t chunks, int state_bits, double lr, dou
     if ((state_bits != 8 && state_bits != 32) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
         !(eps >= 0.0) || !std::isfinite(lr) || step < 1)
         return PMN_EINVAL;
-    if (chunks < 0 || chunks >= ((int64_t)1 << 31)) return PMN_ESHAPE;
+    if (chunks < 0 || chunks >= ADAMW_MOST_CHUNKS) return PMN_ESHAPE;
     if (chunks == 0) return PMN_OK;
     if (!table) return PMN_EINVAL;
     if (!aligned(table, 8) || !aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(grad_scale_dev, 4))

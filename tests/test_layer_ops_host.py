@@ -92,6 +92,7 @@ def test_adamw_table_refusals(lib):
     assert build(entry(), bits=16)[0] == EINVAL and build(entry(n=-1))[0] == ESHAPE
     assert build(entry(), count=-1)[0] == ESHAPE and build(entry(grad_dtype=2))[0] == EINVAL
     assert build(entry(n=(1 << 40) + 1))[0] == ESHAPE
+    assert build(entry(n=1 << 35))[0] == ESHAPE   # 2^24 chunks
     for k in ("param", "grad", "m", "v", "m_e8m0", "v_e8m0"):
         assert build(entry(**{k: None}))[0] == EINVAL, k
     assert build(entry(m_e8m0=None, v_e8m0=None), bits=32)[0] == 0
@@ -106,7 +107,7 @@ def test_adamw_step_refusals(lib):
         return lib.adamw_step(table, chunks, bits, lr, b1, b2, eps, step, lrd, sd, gd, 0, 0, None)
     assert f(bits=4) == EINVAL and f(b1=1.0) == EINVAL and f(b2=-0.1) == EINVAL and f(eps=-1e-9) == EINVAL
     assert f(lr=float("inf")) == EINVAL and f(step=0) == EINVAL and f(b1=float("nan")) == EINVAL
-    assert f(chunks=-1) == ESHAPE and f(chunks=1 << 31) == ESHAPE and f(table=None) == EINVAL
+    assert f(chunks=-1) == ESHAPE and f(chunks=1 << 24) == ESHAPE and f(table=None) == EINVAL
     assert f(table=C.c_void_p(0x1004)) == EALIGN and f(lrd=C.c_void_p(0x1002)) == EALIGN
     assert f(sd=C.c_void_p(0x1004)) == EALIGN and f(gd=C.c_void_p(0x1001)) == EALIGN
     assert f(chunks=0, table=None) == 0
