@@ -53,6 +53,7 @@ struct FfnArgs {
     float* part;            // PART: [splits x Nc x Nr]
     int splits;
     int64_t rtiles, ctiles;
+    int64_t whole;          // tiles that run whole; the others in two halves (ffn_grid)
 };
 
 // The 16-byte words of aux that 8 consecutive outputs n .. n+7 of output row c need: ADD's add, or
@@ -160,6 +161,8 @@ struct FfnTile {
     static constexpr int RPW = BR / 16 / (WR * WC), CPW = BC / 16 / (WR * WC), PPW = RPW + CPW;   // pieces per wavefront
     static constexpr int OPITCH = BR + 4;                       // floats per staged output row
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
+    static constexpr bool HALVES = RB_ * CB_ == 16;
+    typedef FfnTile<WR_, WC_, RB_, CB_ / 2, NST_> Half;         // of the output rows, all of the columns
     static constexpr bool PAIRS = RPW % 2 == 0 && CPW % 2 == 0;
     static constexpr int RING = (PAIRS ? 5 : NST) * STAGE, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
@@ -167,19 +170,22 @@ struct FfnTile {
     static_assert((PAIRS ? 6 : NST - 1) * PPW <= 63, "vmcnt");
 };
 
-// Tile i of a product's rtiles x ctiles for workgroup L: workgroups L, L + 8, .. run on one XCD and take
-// consecutive tiles, in bands of 8 tile rows walked down their columns, so that the 32 tiles of an XCD at
-// a time share 8 + 4 operand panels in its L2. False past the last tile.
-PMN_DEV bool ffn_tile_of(const FfnArgs& p, int64_t L, int64_t& trow, int64_t& tcol)
+// Item number of workgroup L among n: workgroups L, L + 8, .. run on one XCD and take consecutive items.
+// Negative past the last.
+PMN_DEV int64_t ffn_item_of(int64_t n, int64_t L)
 {
-    const int64_t total = p.rtiles * p.ctiles, per = (total + 7) >> 3;
-    const int64_t i = (L & 7) * per + (L >> 3);
-    if ((L >> 3) >= per || i >= total) return false;
+    const int64_t per = (n + 7) >> 3, i = (L & 7) * per + (L >> 3);
+    return (L >> 3) >= per || i >= n ? -1 : i;
+}
+
+// Tile i of a product's rtiles x ctiles: in bands of 8 tile rows walked down their columns, so that the
+// 32 tiles of an XCD at a time share 8 + 4 operand panels in its L2.
+PMN_DEV void ffn_tile_at(const FfnArgs& p, int64_t i, int64_t& trow, int64_t& tcol)
+{
     const int64_t band = i / (8 * p.ctiles), in = i - band * 8 * p.ctiles;
     const int64_t height = p.rtiles - band * 8 < 8 ? p.rtiles - band * 8 : 8;
     tcol = in / height;
     trow = band * 8 + (in - tcol * height);
-    return true;
 }
 
 // The tile (trow, tcol) of a product, or part `split` of its contraction (PART).
@@ -483,8 +489,22 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
         L /= p.splits;
         trow = L % p.rtiles;
         tcol = L / p.rtiles;
-    } else if (!ffn_tile_of(p, L, trow, tcol)) {
-        return;
+    } else {
+        if constexpr (T::HALVES) {
+            // whole: all tiles, which need not fill the grid's last 8 workgroups, or a multiple of 256
+            const int64_t rest = p.rtiles * p.ctiles - p.whole;
+            if (rest > 0 && L >= p.whole) {
+                const int64_t h = ffn_item_of(2 * rest, L - p.whole);
+                if (h < 0) return;
+                ffn_tile_at(p, p.whole + (h >> 1), trow, tcol);
+                tcol = 2 * tcol + (h & 1);
+                if (tcol * (T::BC / 2) < p.Nc) ffn_tile<typename T::Half, RKC, CKC, EPI>(p, trow, tcol, 0, lds);
+                return;
+            }
+        }
+        const int64_t i = ffn_item_of(T::HALVES ? p.whole : p.rtiles * p.ctiles, L);
+        if (i < 0) return;
+        ffn_tile_at(p, i, trow, tcol);
     }
     ffn_tile<T, RKC, CKC, EPI>(p, trow, tcol, split, lds);
 }
@@ -507,7 +527,9 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_ffn
     const uint32_t first = w == 0 ? 0u : w == 1 ? a.end[0] : a.end[1];
     const FfnArgs& p = a.p[w];
     int64_t trow, tcol;
-    if (!ffn_tile_of(p, L - first, trow, tcol)) return;
+    const int64_t i = ffn_item_of(p.rtiles * p.ctiles, L - first);
+    if (i < 0) return;
+    ffn_tile_at(p, i, trow, tcol);
     if (w == a.dx) ffn_tile<T, false, true, FFN_BF16>(p, trow, tcol, 0, lds);
     else ffn_tile<T, false, false, DW>(p, trow, tcol, 0, lds);
 }
@@ -667,21 +689,28 @@ static int64_t ffn_part_floats(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
     return (int64_t)ffn_plan(Nc, Nr, K, ckc).splits * Nc * Nr;
 }
 
-// Tile grid of a product; returns its workgroups (a multiple of 8, without PART)
+// Tile grid of a product; returns its workgroups (a multiple of 8, without PART). Where 256 x 256 tiles
+// leave a last round with up to half of the CUs at work, that round's tiles go in halves to all of them
+// (8192 x 7168 x 2048 forward, whose w2 product has 896: 621 -> 607 us); a fuller round would not fit in
+// halves.
+// halves: false in the gradients' launch, whose products fill each other's rounds.
 template <typename T, int EPI>
-static int64_t ffn_grid(FfnArgs& p)
+static int64_t ffn_grid(FfnArgs& p, bool halves)
 {
     const int64_t nr = EPI == FFN_SWIGLU ? p.F : p.Nr, br = EPI == FFN_SWIGLU ? T::BR / 2 : T::BR;
     p.rtiles = (nr + br - 1) / br;
     p.ctiles = (p.Nc + T::BC - 1) / T::BC;
     const int64_t n = p.rtiles * p.ctiles;
-    return EPI == FFN_PART ? n * p.splits : (n + 7) / 8 * 8;
+    if (EPI == FFN_PART) return n * p.splits;
+    const int64_t rest = n % FFN_CUS;
+    p.whole = T::HALVES && halves && rest > 0 && rest <= FFN_CUS / 2 ? n - rest : n;
+    return p.whole < n ? p.whole + (2 * rest + 7) / 8 * 8 : (n + 7) / 8 * 8;
 }
 
 template <typename T, bool RKC, bool CKC, int EPI>
 static void ffn_launch_tile(FfnArgs p, hipStream_t stream)
 {
-    const int64_t grid = ffn_grid<T, EPI>(p);
+    const int64_t grid = ffn_grid<T, EPI>(p, true);
     hipLaunchKernelGGL((k_ffn_gemm<T, RKC, CKC, EPI>), dim3((unsigned)grid), dim3(T::THREADS), 0, stream, p);
 }
 
@@ -701,7 +730,7 @@ static void ffn_launch_grads(const FfnArgs* p, int count, int dx, hipStream_t st
         if (i < count) {
             a.p[i] = p[order[i]];
             if (order[i] == dx) a.dx = i;
-            end += ffn_grid<T, FFN_BF16>(a.p[i]);
+            end += ffn_grid<T, FFN_BF16>(a.p[i], false);
         }
         a.end[i] = (uint32_t)end;
     }

@@ -247,8 +247,10 @@ def test_streams_and_graph(P, M):
         assert all(torch.equal(a, b) for a, b in zip(out, call())), f"replay {k}"
 
 
-# sizes that reach the 256 x 256 tiles (160 of them and more), ragged at every edge; fp64 on the GPU
-@pytest.mark.parametrize("M,H,F", [(2600, 264, 2056), (2600, 4104, 72), (1300, 2056, 1288)])
+# sizes that reach the 256 x 256 tiles (160 of them and more), ragged at every edge; 4200 and 4260 rows have
+# 289, the last 33 in halves of 128 rows, with 104 rows of the last one left or 164; fp64 on the GPU
+@pytest.mark.parametrize("M,H,F", [(2600, 264, 2056), (2600, 4104, 72), (1300, 2056, 1288), (4260, 4104, 72),
+                                   (4200, 4104, 72), (4200, 72, 2056)])
 def test_forward_of_many_tiles(P, M, H, F):
     d = dev(case(M, H, F, M + H + F))
     h, hb, y, yb = ref_fwd(d)
@@ -257,7 +259,7 @@ def test_forward_of_many_tiles(P, M, H, F):
     within(got, y, yb, "y")
 
 
-@pytest.mark.parametrize("M,H,F", [(5000, 2600, 2056), (5000, 5000, 1032), (3000, 264, 136), (9000, 72, 264)])
+@pytest.mark.parametrize("M,H,F", [(5000, 2600, 2056), (5000, 5000, 1032), (3000, 264, 136), (9000, 72, 264), (4200, 72, 4104)])
 def test_backward_of_many_tiles(P, M, H, F):
     d = dev(bwd_case(M, H, F, M + H + F))
     ref = ref_bwd(d)
