@@ -664,23 +664,32 @@ struct FfnPlan {
     int splits;    // 0: no split
 };
 
-// Tile and split of a product of Nc x Nr outputs over K.
+// Tile and split of a product of Nc x Nr outputs over K. The small tiles split the contraction so that
+// one workgroup, and no second one, goes to each CU: parts that leave a few CUs with two cost the length
+// of one more (rounded up, not down: 384 rows of 7168 x 2048 forward 77 us against 61, 640 rows of 1024 x
+// 2048 40 against 28). Large tiles from half a round of them: 128 x 128 ones would take 3000 rows of 4096 x
+// 1536 140 us against 124; below that they are faster. 128 x 64 tiles, whose fewer parts are shorter to
+// add but which load 1.5 times the bytes, where they are split in two or more, or three for a long
+// contraction: 200 rows of 4096 x 1536 39 us against 34; with two parts of 7168, 160 rows of 7168 x 2048
+// 43 us against 47.
 static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
 {
     if (Nc == 0) return {1, 0};
     auto tiles = [&](int64_t br, int64_t bc) { return ((Nr + br - 1) / br) * ((Nc + bc - 1) / bc); };
     const int64_t stages = (K + 31) / 32;
-    auto split_for = [&](int64_t t, int64_t want, int64_t least) {
-        int64_t s = (want + t - 1) / t;
+    auto split_for = [&](int64_t t, int64_t least) {
+        int64_t s = FFN_CUS / t;
         const int64_t most = stages / least;
         s = s > most ? most : s;
         return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
     };
-    if (ckc && Nc <= 64) return {2, split_for(tiles(128, 64), FFN_CUS, 8)};
-    if (tiles(256, 256) >= 160) return {0, 0};
+    const int64_t few = tiles(128, 64);
+    if (ckc && (Nc <= 64 || (stages >= 32 && few <= (stages <= 128 ? FFN_CUS / 2 : FFN_CUS / 3))))
+        return {2, split_for(few, 8)};
+    if (tiles(256, 256) >= FFN_CUS / 2) return {0, 0};
     const int64_t t = tiles(128, 128);
     if (t >= FFN_CUS || stages < 32) return {1, 0};
-    const int s = split_for(t, FFN_CUS, 16);
+    const int s = split_for(t, 16);
     return {1, s > 1 ? s : 0};
 }
 
