@@ -314,12 +314,16 @@ hipError_t launch_rmsnorm_fwd(const uint16_t* x, const void* res, bool res_f32, 
 
 // Workgroups of the backward = partial rows of dgamma: enough to fill the chip, few enough that the
 // partials stay small beside the rows (at 1024 they are half of the traffic of 1000 rows: 7168 values
-// wide 22 us, at 512 15). A function of the sizes alone, so results are too.
+// wide 22 us, at 512 15). Rows over 1024 threads fill half of a CU each: up to 1024 of them go to 256
+// workgroups, which halves the partials (fp32 rows of 7168: 640 rows 18.2 us with 512, 16.7 with 256, 850
+// rows 24.0 and 21.1, 1500 rows 36.5 and 37.1; of 4096 over 512 threads: 777 rows 14.4 and 14.7). A
+// function of the sizes alone, so results are too.
 static int64_t rmsnorm_bwd_groups(int64_t rows, int64_t C)
 {
     const int64_t rpb = C <= 2048 ? 4 : 1;
     const int64_t n = (rows + rpb - 1) / rpb;
-    return n < 512 ? n : 512;
+    const int64_t most = C > 4096 && rows <= 1024 ? 256 : 512;
+    return n < most ? n : most;
 }
 
 size_t rmsnorm_bwd_ws_bytes(int64_t rows, int64_t C)
