@@ -533,6 +533,10 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
  * seed + step and stream rng_stream + 2 j (m) or rng_stream + 2 j + 1 (v), its place on the grid taken
  * from value * powf(2, -e) in fp32 (as torch.ldexp scales); a root above zero gets at least the
  * smallest code. The update uses the moments before their rounding.
+ * Values that are not finite stay by themselves. In fp32 a gradient past about 1.8e19 makes its v
+ * infinite, and its weight only decays from then on. In 8 bits a value whose m or v is not finite in
+ * fp32 has NaN codes for both, so its weight is NaN from the next step on; the other values of its
+ * block keep the codes and scales that they have without it.
  */
 typedef struct {
     float* param;         /* [n] */

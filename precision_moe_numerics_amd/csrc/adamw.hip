@@ -9,7 +9,8 @@
 // of its largest v. Both round stochastically (the requant's rule and its index-keyed generator):
 // with b2 near 1 a step changes sqrt(v) by far less than half a code step, so rounding to nearest
 // would never let it decay; in expectation stochastic rounding keeps every change. A root above zero
-// never becomes zero: it would be a denominator of eps alone at the next step.
+// never becomes zero: it would be a denominator of eps alone at the next step. A value whose m or v
+// is not finite keeps NaN in both, and its block the scales that it would have without it.
 // The update itself uses m and v before they are rounded.
 //
 // Bound by HBM traffic (fp32 states: 26 bytes a value read and written plus the gradient; 8 bits:
@@ -122,13 +123,13 @@ PMN_DEV float quad_lane(float v)
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x55 * L, 0xF, 0xF, true));
 }
 
-// Exponent of the E8M0 scale of a block held by the 4 lanes of a quad
-PMN_DEV int block_exponent(const float (&v)[8])
+// Largest magnitude of a block held by the 4 lanes of a quad, NaN left out
+PMN_DEV float block_max(const float (&v)[8])
 {
     float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(v[j]));
-    return e8m0_exponent<E8M0_E4M3>(quad_max4(amax));
+    return quad_max4(amax);
 }
 
 // 8 values of a block of exponent e: stochastic E4M3 codes of v * scale; the quad's first lane writes
@@ -227,7 +228,18 @@ __global__ __launch_bounds__(adw::THREADS) void k_adamw(const AdamwTable* __rest
     if constexpr (EIGHT) {
         const uint64_t seed = a.seed + (uint64_t)step, blk = (uint64_t)i0 >> 3;
         const uint32_t stream = a.rng_stream + 2u * (uint32_t)ck.tensor;
-        const int em = block_exponent(m), ev = block_exponent(root);
+        // An infinity would be its block's scale, and the 31 other values' moments zeros and roots too large
+        // to square: where one is (the same in all lanes of a quad), a value whose m or v is not finite gets
+        // NaN for both, which no scale counts.
+        float am = block_max(m), ar = block_max(root);
+        if (fmaxf(am, ar) == INFINITY) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (!(fabsf(m[j]) < INFINITY && root[j] < INFINITY)) m[j] = root[j] = NAN;
+            am = block_max(m);
+            ar = block_max(root);
+        }
+        const int em = e8m0_exponent<E8M0_E4M3>(am), ev = e8m0_exponent<E8M0_E4M3>(ar);
         // 2^-e of both, one powf a lane: even lanes of a quad take m's, odd ones v's
         const float inv = powf(2.0f, (float)-(threadIdx.x & 1 ? ev : em));
         store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.m_e8m0 + (i0 >> 5), n, m, em, quad_lane<0>(inv), seed,
