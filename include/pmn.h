@@ -531,7 +531,8 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
  * [ceil(n / 32)], MXFP8 over runs of 32 values of m and of sqrt(v) (zero bytes are zero moments),
  * rounded stochastically as the requant rounds: value i of tensor j of the list draws index i under
  * seed + step and stream rng_stream + 2 j (m) or rng_stream + 2 j + 1 (v), its place on the grid taken
- * from value * powf(2, -e) in fp32 (as torch.ldexp scales); a root above zero gets at least the
+ * from value * powf(2, -e) in fp32 (as torch.ldexp scales; never above value * 2^-e, at most one ulp
+ * below it, which costs one of 65536 values on the grid a code); a root above zero gets at least the
  * smallest code. The update uses the moments before their rounding.
  * Values that are not finite stay by themselves. In fp32 a gradient past about 1.8e19 makes its v
  * infinite, and its weight only decays from then on. In 8 bits a value whose m or v is not finite in
