@@ -883,6 +883,7 @@ class AdamWPlan:
                                       C.byref(chunks)), "adamw_table_build")
         self.chunks = chunks.value
         self.table = host.to(dev)
+        self._stream = _raw_stream(at)   # whose memory the table is
 
 
 def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int, torch.Tensor], beta1: float = 0.9,
@@ -898,11 +899,14 @@ def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int,
             dev[name] = v
     _need(grad_scale is None or "grad_scale" in dev, "grad_scale must be a device tensor")
     at = _device_of(plan.table, "the plan")
+    stream = _raw_stream(at)
+    if stream != plan._stream:
+        # a plan dropped while this step is still to run must not give its table's memory away
+        plan.table.record_stream(torch.cuda.current_stream())
     _check(_lib.adamw_step(
         _device_ptr(plan.table, at, "the plan"), plan.chunks, plan.state_bits, 0.0 if "lr" in dev else lr, beta1, beta2,
         eps, 1 if "step" in dev else step, _device_ptr(dev.get("lr"), at, "lr"), _device_ptr(dev.get("step"), at, "step"),
-        _device_ptr(dev.get("grad_scale"), at, "grad_scale"), seed, rng_stream & 0xFFFFFFFF, _raw_stream(at)),
-        "adamw_step")
+        _device_ptr(dev.get("grad_scale"), at, "grad_scale"), seed, rng_stream & 0xFFFFFFFF, stream), "adamw_step")
 
 
 # ---- measurement kernels of include/pmn_probe.h ---------------------------------------------

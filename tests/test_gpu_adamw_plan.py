@@ -1,0 +1,40 @@
+"""What an AdamWPlan keeps: its table's memory while steps on other streams still read it, and the
+tensors that the table points to.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def P():
+    import precision_moe_numerics_amd as P
+    return P
+
+
+def test_a_dropped_plan_keeps_its_table_for_a_step_on_another_stream(P):
+    """A plan of one stream, stepped on another that is behind other work and dropped at once: its table's
+    memory is not handed out on the first stream before that step has run, and the step is the usual one."""
+    n = 200_000
+    p, g = torch.randn(n, device=DEV), torch.randn(n, device=DEV)
+    want = P.AdamWTensor.new(p.clone(), g, 32)
+    P.adamw_step(P.AdamWPlan([want]), lr=1e-3, step=1)
+    t = P.AdamWTensor.new(p.clone(), g, 32)
+    plan = P.AdamWPlan([t])
+    at, size = plan.table.data_ptr(), plan.table.numel()
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            busy = torch.mm(busy, busy).mul_(1e-2)
+        P.adamw_step(plan, lr=1e-3, step=1)
+    del plan
+    taken = [torch.empty(size, dtype=torch.int64, device=DEV) for _ in range(8)]
+    assert not side.query(), "the step had already run"
+    assert at not in [x.data_ptr() for x in taken]
+    torch.cuda.synchronize()
+    assert torch.equal(t.param, want.param) and torch.equal(t.v, want.v)
