@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import List, Optional, Union
 
 import torch
@@ -808,6 +808,13 @@ class AdamWTensor:
     v_e8m0: Optional[torch.Tensor] = None
     weight_decay: float = 0.0
 
+    _replaced = 0   # fields set anew, over all instances: plans look at theirs again where it has grown
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            AdamWTensor._replaced += 1
+        object.__setattr__(self, name, value)
+
     @staticmethod
     def new(param: torch.Tensor, grad: torch.Tensor, state_bits: int = 32, copy: Optional[torch.Tensor] = None,
             weight_decay: float = 0.0) -> "AdamWTensor":
@@ -826,11 +833,15 @@ class _AdamWEntry(C.Structure):
 
 
 class AdamWPlan:
-    """A list of tensors to be updated together, as a table on their device, built once and kept (with
-    the tensors) for every step. All of one state width; no tensor twice."""
+    """A list of tensors to be updated together, as a table on their device, built once and kept for
+    every step. All of one state width; no tensor twice. The table holds addresses: the plan keeps the
+    tensors that it was built of, gradients are written into theirs, and a field of an AdamWTensor that is
+    set anew needs another plan (steps of this one are refused)."""
 
     def __init__(self, tensors: List[AdamWTensor]):
         self.tensors = list(tensors)
+        self._built_of = [(t, [(f.name, getattr(t, f.name)) for f in fields(t)]) for t in self.tensors]
+        self._replaced = AdamWTensor._replaced
         _need(len(self.tensors) > 0, "an AdamWPlan needs at least one tensor")
         dev = self.tensors[0].param.device
         self.state_bits = 8 if self.tensors[0].m.dtype == torch.uint8 else 32
@@ -885,6 +896,14 @@ class AdamWPlan:
         self.table = host.to(dev)
         self._stream = _raw_stream(at)   # whose memory the table is
 
+    def _check_tensors(self):
+        for i, (t, built_of) in enumerate(self._built_of):
+            for what, v in built_of:
+                now = getattr(t, what)
+                _need(now is v or (what == "weight_decay" and now == v),
+                      f"tensors[{i}].{what} is not what the plan was built of")
+        self._replaced = AdamWTensor._replaced
+
 
 def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int, torch.Tensor], beta1: float = 0.9,
                beta2: float = 0.95, eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None, seed: int = 0,
@@ -898,6 +917,8 @@ def adamw_step(plan: AdamWPlan, lr: Union[float, torch.Tensor], step: Union[int,
             _need(v.dtype == dt and v.numel() == 1, f"{name} must be one value of {dt}")
             dev[name] = v
     _need(grad_scale is None or "grad_scale" in dev, "grad_scale must be a device tensor")
+    if plan._replaced != AdamWTensor._replaced:
+        plan._check_tensors()
     at = _device_of(plan.table, "the plan")
     stream = _raw_stream(at)
     if stream != plan._stream:

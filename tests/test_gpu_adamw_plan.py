@@ -38,3 +38,35 @@ def test_a_dropped_plan_keeps_its_table_for_a_step_on_another_stream(P):
     assert at not in [x.data_ptr() for x in taken]
     torch.cuda.synchronize()
     assert torch.equal(t.param, want.param) and torch.equal(t.v, want.v)
+
+
+def test_a_replaced_tensor_needs_another_plan(P):
+    """A field set anew after the plan was built is refused, not left unread, until it is set back or
+    planned again; other plans go on, and what the table points to stays allocated."""
+    n = 4096
+    a, b = (P.AdamWTensor.new(torch.randn(n, device=DEV), torch.randn(n, device=DEV), 32) for _ in range(2))
+    plan, other = P.AdamWPlan([a]), P.AdamWPlan([b])
+    P.adamw_step(plan, lr=1e-3, step=1)
+    was, at = a.grad, a.grad.data_ptr()
+    a.grad = torch.randn(n, device=DEV)
+    before = a.param.clone()
+    for _ in range(2):
+        with pytest.raises(P.PmnError, match=r"tensors\[0\].grad"):
+            P.adamw_step(plan, lr=1e-3, step=2)
+    P.adamw_step(other, lr=1e-3, step=1)
+    assert torch.equal(a.param, before)
+    ref = P.AdamWTensor(before.clone(), a.grad, a.m.clone(), a.v.clone())
+    P.adamw_step(P.AdamWPlan([a]), lr=1e-3, step=2)
+    P.adamw_step(P.AdamWPlan([ref]), lr=1e-3, step=2)
+    assert torch.equal(a.param, ref.param)
+    fresh, a.grad = a.grad, was
+    P.adamw_step(plan, lr=1e-3, step=3)
+    a.weight_decay = 0.5
+    with pytest.raises(P.PmnError, match="weight_decay"):
+        P.adamw_step(plan, lr=1e-3, step=4)
+    a.weight_decay = 0.0 * n
+    P.adamw_step(plan, lr=1e-3, step=4)
+    a.grad = fresh
+    del was
+    torch.cuda.synchronize()
+    assert at not in [torch.empty(n, device=DEV).data_ptr() for _ in range(4)]
