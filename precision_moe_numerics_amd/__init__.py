@@ -698,9 +698,10 @@ def rmsnorm_residual_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6
 
 def rmsnorm_residual_bwd(dy: torch.Tensor, z: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
                          dres: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                         dz: Optional[torch.Tensor] = None):
+                         dz: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None):
     """Backward of rmsnorm_residual_fwd: z its residual stream (x where there was no residual), dres the
-    gradient that reaches z along the stream. Returns (dz [rows, cols] of z's type, dgamma fp32 [cols])."""
+    gradient that reaches z along the stream; dz (it may be dres itself) and dgamma (the gradient of an
+    AdamWTensor, for one) may be given. Returns (dz [rows, cols] of z's type, dgamma fp32 [cols])."""
     _need(z.dim() == 2, "z must be [rows, cols]")
     R, Cc = z.shape
     zcode, dcode = _dtype_code(z, "z"), _dtype_code(dy, "dy")
@@ -711,10 +712,12 @@ def rmsnorm_residual_bwd(dy: torch.Tensor, z: torch.Tensor, gamma: torch.Tensor,
         _tensor(dres, (R, Cc), z.dtype, "dres")
     if dz is not None:
         _tensor(dz, (R, Cc), z.dtype, "dz")
+    if dgamma is not None:
+        _tensor(dgamma, (Cc,), torch.float32, "dgamma")
     at = _device_of(z, "z")
     dz = torch.empty_like(z) if dz is None else dz
     workspace = _workspace(workspace, _lib.rmsnorm_residual_bwd_workspace_size(R, Cc), z.device)
-    dgamma = torch.empty_like(gamma)
+    dgamma = torch.empty_like(gamma) if dgamma is None else dgamma
     _check(_lib.rmsnorm_residual_bwd(
         _device_ptr(dy, at, "dy"), dcode, _device_ptr(z, at, "z"), zcode, _device_ptr(gamma, at, "gamma"),
         _device_ptr(rstd, at, "rstd"), _device_ptr(dres, at, "dres"), R, Cc, _device_ptr(dz, at, "dz"),

@@ -70,3 +70,41 @@ def test_a_replaced_tensor_needs_another_plan(P):
     del was
     torch.cuda.synchronize()
     assert at not in [torch.empty(n, device=DEV).data_ptr() for _ in range(4)]
+
+
+def test_the_norms_gradient_goes_to_the_planned_buffer(P):
+    """dgamma written where the plan reads it, over several steps and in a replayed graph: the same weights
+    as with the gradient copied there."""
+    rows, cols = 300, 520
+    z = torch.randn((rows, cols), device=DEV).to(torch.bfloat16)
+    dy = torch.randn((rows, cols), device=DEV).to(torch.bfloat16)
+
+    def program(copied):
+        gamma, grad = torch.ones(cols, device=DEV), torch.zeros(cols, device=DEV)
+        plan = P.AdamWPlan([P.AdamWTensor.new(gamma, grad, 32)])
+        count = torch.ones(1, dtype=torch.int64, device=DEV)
+
+        def step():
+            o = P.rmsnorm_residual_fwd(z, gamma, want_rstd=True)
+            if copied:
+                grad.copy_(P.rmsnorm_residual_bwd(dy, z, gamma, o.rstd)[1])
+            else:
+                assert P.rmsnorm_residual_bwd(dy, z, gamma, o.rstd, dgamma=grad)[1] is grad
+            P.adamw_step(plan, lr=1e-2, step=count)
+            count.add_(1)
+        return step, gamma
+
+    (by_copy, a), (given, b), (captured, c) = program(True), program(False), program(False)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured()
+    for _ in range(3):
+        by_copy()
+        given()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(a, c) and not (a == 1).any()
+    buf = torch.empty(cols + 8, device=DEV).fill_(7.0)
+    P.rmsnorm_residual_bwd(z[:0], z[:0], a, torch.empty(0, device=DEV), dgamma=buf[4:-4])
+    assert (buf[4:-4] == 0).all() and (buf[:4] == 7).all() and (buf[-4:] == 7).all()
