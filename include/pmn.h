@@ -466,7 +466,9 @@ int pmn_check_indices(const int64_t* offsets, int G, int64_t M, const int32_t* g
  *   z = x + residual, s = 1 / sqrt(mean(z^2) + eps) per row, y = z s gamma.
  * residual: NULL (z = x; z_out is not used), or [rows x cols] of res_dtype (PMN_DTYPE_*), and then
  *   z_out, of the same type, receives z (it may be residual itself). y is computed from z itself.
- * gamma: fp32 [cols]. Outputs, each nullable but at least one of y and codes given: y bf16
+ * gamma: fp32 [cols]; where it is infinite y is infinite or NaN. An s past fp32's range (eps 0, and a row
+ *   of zeros or subnormals) is infinite, and its row NaN.
+ * Outputs, each nullable but at least one of y and codes given: y bf16
  *   [rows x cols]; codes uint8 [rows x cols] and e8m0 uint8 [rows x cols/32], the row-wise MXFP8 form
  *   of y before any rounding to bf16 (scale rule and rounding to nearest even as mxfp8_quantize; a NaN
  *   or infinite y has a NaN code, 0x7F or 0xFF); rstd fp32 [rows], s for the backward.

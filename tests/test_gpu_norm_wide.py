@@ -123,3 +123,24 @@ def test_outputs_to_the_last_bits(P, rows, cols, res):
     assert (torch.minimum((top - 1).abs(), (2 * top - 1).abs()) <= 2 * slack).all()
     same = ~other
     within(got[same], t[same], step[same] / 2 + slack * t[same].abs(), "codes")
+
+
+def test_infinite_gamma_and_norms_past_the_range(P):
+    """An infinite gamma makes its column infinite or NaN and leaves the others alone; a row whose
+    1 / norm passes fp32 (eps 0, zeros or subnormals) has an infinite rstd and is NaN, the other rows are
+    what they are."""
+    rows, cols = 9, 264
+    s, g = stream_like(rows, cols, 3)
+    x = s.to(torch.bfloat16)
+    gamma = 1.0 + 0.1 * torch.randn(cols, generator=g, device=DEV)
+    odd = gamma.clone()
+    odd[8], odd[263] = float("inf"), -float("inf")
+    a, b = P.rmsnorm_residual_fwd(x, gamma), P.rmsnorm_residual_fwd(x, odd)
+    keep = torch.isfinite(odd)
+    assert torch.equal(a.y[:, keep], b.y[:, keep]) and not torch.isfinite(b.y[:, ~keep]).any()
+    x[3], x[7] = 0.0, 1e-40
+    a = P.rmsnorm_residual_fwd(x, gamma, 0.0, want_rstd=True)
+    rest = [0, 1, 2, 4, 5, 6, 8]
+    alone = P.rmsnorm_residual_fwd(x[rest].contiguous(), gamma, 0.0)
+    assert torch.equal(a.y[rest], alone.y) and torch.isfinite(alone.y).all()
+    assert torch.isinf(a.rstd[[3, 7]]).all() and torch.isnan(a.y[[3, 7]]).all()
