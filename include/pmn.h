@@ -471,7 +471,8 @@ int pmn_check_indices(const int64_t* offsets, int G, int64_t M, const int32_t* g
  * Outputs, each nullable but at least one of y and codes given: y bf16
  *   [rows x cols]; codes uint8 [rows x cols] and e8m0 uint8 [rows x cols/32], the row-wise MXFP8 form
  *   of y before any rounding to bf16 (scale rule and rounding to nearest even as mxfp8_quantize; a NaN
- *   or infinite y has a NaN code, 0x7F or 0xFF); rstd fp32 [rows], s for the backward.
+ *   or infinite y has a NaN code, 0x7F or 0xFF), for a caller's own 8-bit products (the grouped calls here
+ *   take bf16 or NVFP4 and quantize themselves); rstd fp32 [rows], s for the backward.
  * cols % 8 == 0 (with codes: cols % 32 == 0), cols <= 32768, rows < 2^31 (PMN_ESHAPE); eps >= 0
  * (PMN_EINVAL); every pointer 16-byte aligned but e8m0 (any) and rstd (4) (PMN_EALIGN).
  */

@@ -133,9 +133,9 @@ PMN_DEV float block_max(const float (&v)[8])
 }
 
 // 2^-e as torch.ldexp forms it, by powf, so that states packed by torch operations have the same codes.
-// powf is one ulp low for some e (some), where one of 65536 values on the grid gets the code
-// below it; it is held to 2^-e, for one ulp high would put a block's largest value past 448. (The exact
-// power: 460 us for 150 M values against 464.)
+// powf is one ulp low for some e, where one of 65536 values on the grid gets the code below it; it is
+// held to 2^-e, for one ulp high would put a block's largest value past 448. (The exact power: 460 us for
+// 150 M values against 464.)
 PMN_DEV float block_scale(int e) { return fminf(powf(2.0f, (float)-e), __builtin_ldexpf(1.0f, -e)); }
 
 // 8 values of a block of exponent e: stochastic E4M3 codes of v * scale; the quad's first lane writes

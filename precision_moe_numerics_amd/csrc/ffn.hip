@@ -24,6 +24,11 @@
 //     ((k / 8) % 2) | 2 (k % 4), so that the 4 k of 16 lanes lie in different banks (174 B/clk/CU
 //     measured; 64 without).
 //
+// a and dh13 are rounded to bf16 between the products, whose operands the bf16 MFMAs take (at most
+// 2^-8 of a value; a second MFMA for what is rounded off would double those products): y and the gradients are
+// off by 0.0021 to 0.0024 in norm, of which the rounding of the outputs themselves is 0.0017. h13 is stored
+// in bf16; the forward's own a comes from the fp32 sums.
+//
 // The accumulators leave through LDS, 32 output rows of a wavefront column at a time, so that a
 // thread finishes 8 consecutive values of an output row with 16-byte accesses. Where the tiles of a
 // product are fewer than the compute units the contraction is split: the parts write fp32 sums and a
@@ -248,7 +253,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
     // An operand's bytes from its first at stage 0 of this part, a stage's advance and how many bytes
-    // there are (a k-contiguous operand is bounded by rows and chunks instead)
+    // there are. A k-contiguous operand is bounded by the lanes' row and chunk checks alone, which hold for
+    // this base and no other: its own byte count as a second bound took 10 to 30% of the forward, counted
+    // in 32 bits 1 to 4%.
     struct Operand {
         const uint8_t* base;
         int64_t step, bytes;
@@ -569,7 +576,7 @@ __global__ __launch_bounds__(256) void k_ffn_reduce(FfnArgs p)
 // through LDS: one launch, no workspace. Columns past Nc repeat the last row and are not stored. Each
 // workgroup reads all of C from L2, so beyond 16 rows the ring's tiles with a split contraction are
 // faster (32 rows of 7168 x 2048: 35 us, this kernel with two column tiles 42).
-// One row of 7168 x 2048 (88 MB of weights): 12.6 us and 6.9 us, 4.7 and 4.3 TB/s.
+// One row of 7168 x 2048 (88 MB of weights): 12.9 us and 7.8 us, 4.5 and 3.8 TB/s.
 template <int EPI>
 __global__ __launch_bounds__(512, 2) void k_ffn_few(FfnArgs p)
 {
@@ -671,7 +678,8 @@ struct FfnPlan {
 // 1536 140 us against 124; below that they are faster. 128 x 64 tiles, whose fewer parts are shorter to
 // add but which load 1.5 times the bytes, where they are split in two or more, or three for a long
 // contraction: 200 rows of 4096 x 1536 39 us against 34; with two parts of 7168, 160 rows of 7168 x 2048
-// 43 us against 47.
+// 43 us against 47. (Rounding down leaves CUs idle where a product has 129 to 255 tiles: 768 rows of 7168 x
+// 2048 take 102 us where rounding up took 97, 1024 rows 112 against 110.)
 static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
 {
     if (Nc == 0) return {1, 0};
@@ -800,7 +808,10 @@ hipError_t launch_ffn_fwd(const uint16_t* x, const uint16_t* w13, const uint16_t
 
 // Tile of the gradients' one launch, -1 for a launch each with split contractions. One launch where
 // its workgroups fill the chip and the longest contraction is not much longer than their share of it:
-// with few tiles of a long one (small weights, many tokens) splitting them is faster.
+// with few tiles of a long one (small weights, many tokens) splitting them is faster. 256 x 256 tiles from
+// 640 of them, two and a half rounds: 7 to 17% faster than 128 x 128 ones at 640 to 944 (4096 rows of 4096 x
+// 2048: 377 us against 411). Below, from 416 on, between 3% slower (2000 rows of 7168 x 1024, 560 tiles: 209
+// us against 203) and 13% faster (3100 of 4096 x 1536, 496: 233 against 267), at 304 to 320 7 to 11% slower.
 static int ffn_grads_tile(int64_t M, int64_t H, int64_t F, bool dgrad, bool wgrad)
 {
     if (M == 0) return 1;

@@ -11,8 +11,8 @@
 //
 // Both are bound by HBM traffic: every value is read once into registers (a row is held by one
 // wavefront, 512 or 1024 threads, in 16-byte pieces of 8 values) and written once: 16384 rows of 4096
-// with a bf16 residual move 606 MB forward (y and codes out) in 107 us, 537 MB backward in 107 us, 5.7
-// and 5.0 TB/s where a copy of 1 GB reaches 5.1. Sums (fp64 forward, fp32 backward) take a thread's
+// with a bf16 residual move 606 MB forward (y and codes out) in 104 us, 537 MB backward in 104 us, 5.8
+// and 5.2 TB/s where a copy of 1 GB reaches 5.1. Sums (fp64 forward, fp32 backward) take a thread's
 // values in order, then a butterfly over the lanes, then the wavefronts in order, so results do not
 // depend on the launch.
 #include "pmn_dev.hpp"
@@ -315,9 +315,12 @@ hipError_t launch_rmsnorm_fwd(const uint16_t* x, const void* res, bool res_f32, 
 // Workgroups of the backward = partial rows of dgamma: enough to fill the chip, few enough that the
 // partials stay small beside the rows (at 1024 they are half of the traffic of 1000 rows: 7168 values
 // wide 22 us, at 512 15). Rows over 1024 threads fill half of a CU each: up to 1024 of them go to 256
-// workgroups, which halves the partials (fp32 rows of 7168: 640 rows 18.2 us with 512, 16.7 with 256, 850
-// rows 24.0 and 21.1, 1500 rows 36.5 and 37.1; of 4096 over 512 threads: 777 rows 14.4 and 14.7). A
-// function of the sizes alone, so results are too.
+// workgroups, which halves the partials. 512 against 256 workgroups, us (rows of 4104 to 32768 values,
+// 300 to 1024 of them, in either type: never more than 2% slower with 256):
+//     bf16  640 x 4608 12.0, 11.8   640 x 7168 14.0, 12.7   1024 x 12288 27.0, 23.5   1024 x 32768 83.7, 71.4
+//     fp32  640 x 4608 13.7, 13.1   640 x 7168 19.9, 17.4   1024 x 12288 42.8, 36.5   1024 x 32768 157, 142
+// 2500 rows go the other way up to 8192 values (bf16 of 4608 19.7, 21.7), and so do shorter rows (fp32 of
+// 4096 over 512 threads: 777 rows 14.4, 14.7). A function of the sizes alone, so results are too.
 static int64_t rmsnorm_bwd_groups(int64_t rows, int64_t C)
 {
     const int64_t rpb = C <= 2048 ? 4 : 1;

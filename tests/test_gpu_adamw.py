@@ -1,6 +1,6 @@
 """adamw_step against fp64, and its 8-bit states against the oracle's random numbers.
 
-Tolerances, with u = 2^-24. m and v are a product and an fma each: off by at most 4 u of the sum of
+Tolerances, with u = 2^-24. m and v are products and a sum, each rounded: off by at most 4 u of the sum of
 their terms' magnitudes. The update's root, quotient, products and its rounded scalars stay within
 16 u of it, and m's error passes through it: |p - ref| <= 2 u |p| + lr (16 u |upd| + E_m / d) where
 d is the denominator. States in 8 bits: a value lies between two neighbours of the E4M3 grid of its

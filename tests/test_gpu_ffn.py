@@ -247,8 +247,9 @@ def test_streams_and_graph(P, M):
         assert all(torch.equal(a, b) for a, b in zip(out, call())), f"replay {k}"
 
 
-# sizes that reach the 256 x 256 tiles (160 of them and more), ragged at every edge; 4200 and 4260 rows have
-# 289, the last 33 in halves of 128 rows, with 104 rows of the last one left or 164; fp64 on the GPU
+# sizes around the 256 x 256 tiles (128 of them and more; 1300 rows have 66 and take 128 x 128 ones), ragged
+# at every edge; 4200 and 4260 rows have 289, the last 33 in halves of 128 rows, with 104 rows of the last
+# one left or 164; fp64 on the GPU
 @pytest.mark.parametrize("M,H,F", [(2600, 264, 2056), (2600, 4104, 72), (1300, 2056, 1288), (4260, 4104, 72),
                                    (4200, 4104, 72), (4200, 72, 2056)])
 def test_forward_of_many_tiles(P, M, H, F):

@@ -1,12 +1,13 @@
 """rmsnorm_residual_fwd / _bwd against fp64.
 
-Tolerances, with u = 2^-24. Forward: a thread adds at most 32 squares, 6 butterfly steps and 16
-wavefronts follow, z itself is off by u, so the sum of squares is off by at most 57 u of itself and
-1 / sqrt by 32 u; y adds z's rounding and two products: 40 u covers them. Stored values add half a
-step of their type (bf16 2^-8, fp32 u; E4M3 2^-4, or 2^-10 of the block's scale below its normal
-range). Backward: the row's dot product is off by at most 60 u of S = mean|t xh|, so
-|dz - ref| <= 64 u (s (|t| + |xh| S) + |dres|) + half a step; dgamma adds at most rows / 1024 + 4 + 80
-terms in a row: 128 u sum|dy xh| for the rows tested here.
+Tolerances, with u = 2^-24. Forward: wide enough for sums in fp32 (at most 32 squares a thread, 6
+butterfly steps and 16 wavefronts, z itself off by u: 57 u of the sum, 32 u of 1 / sqrt; z's rounding and
+two products in y: 40 u in all); the kernel's are in fp64, and test_gpu_norm_wide.py holds them to it.
+Stored values add half a step of their type (bf16 2^-8, fp32 u; E4M3 2^-4, or 2^-10 of the block's scale
+below its normal range). Backward: the row's dot product is off by at most 60 u of S = mean|t xh|, so
+|dz - ref| <= 64 u (s (|t| + |xh| S) + |dres|) + half a step; dgamma adds the rows that a thread takes (of
+those tested here at most 3 of 2048 values and less, one of more), 3 groups of a workgroup, up to 16
+partial rows and 32 sums: 128 u sum|dy xh| covers them.
 """
 import numpy as np
 import pytest
