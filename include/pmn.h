@@ -435,6 +435,94 @@ int moe_combine_s2f6(const int8_t* codes, const uint8_t* e8m0, int64_t M, int64_
                      pmn_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* The expert layer on unquantized activations: products grouped by expert in bf16, products of  */
+/* a few tokens with NVFP4 weights, and the sum of the experts' rows with its gradient.          */
+/* ------------------------------------------------------------------------------------------ */
+
+/*
+ * moe_grouped_gemm_fwd in bf16, for layers that stay unquantized and as what the quantized ones are
+ * compared with:
+ *   Y[s, n] = sum_k x[row_s, k] w[g*N + n, k]   (exact products, fp32 accumulation)
+ * x bf16 [x_rows x K], w bf16 [G*N x K], s a slot of group g (offsets, device int64 [G+1], offsets[G] = M)
+ * and row_s = gather[s] (device int32 [M]) or s (then M <= x_rows). epilogue PMN_EPI_F32, _BF16 or _SWIGLU
+ * (PMN_EINVAL otherwise), whose outputs are those of moe_grouped_gemm_fwd: out [M x N], or bf16 [M x F] =
+ * silu(h1) h3 with out_aux NULL or bf16 [M x N] = h1 | h3.
+ * N % 8 == 0 (SWIGLU: N % 16 == 0), K % 8 == 0, N and K <= 2^20, M < 2^31, and no more of them than one
+ * launch holds (PMN_ESHAPE). x, w, out and out_aux 16-byte aligned (PMN_EALIGN). M == 0 launches nothing.
+ */
+int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gather, const void* w,
+                              const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out,
+                              void* out_aux, pmn_stream_t stream);
+
+/*
+ * Its backward from dy bf16 [M x N]:
+ *   PMN_BWD_DGRAD: da[s, k] = sum_n dy[s, n] w[g*N + n, k], [M x K] of da_dtype (PMN_DTYPE_*)
+ *   PMN_BWD_WGRAD: db[g*N + n, k] = sum_{s in g} dy[s, n] x[row_s, k], [G*N x K] of db_dtype; zeros for a
+ *     group without slots
+ * flags: DGRAD, WGRAD or both (PMN_EINVAL otherwise). da is a slot's gradient: moe_combine_rows_fwd without
+ * gates adds a token's slots.
+ * h13 (NULL, or bf16 [M x 2K]: the h1 | h3 that moe_grouped_gemm_fwd_bf16 saved before a product with these
+ * weights, whose input was x = silu(h1) h3): the gradient goes on through the SwiGLU, and da is instead
+ * dh13 bf16 [M x 2K] = da h3 silu'(h1) | da silu(h1), formed from the fp32 da. Then x may be NULL: wgrad takes
+ * silu(h1) h3, rounded to bf16, from h13. With h13: DGRAD set, no gather, da_dtype bf16 (PMN_EINVAL).
+ * Sizes and alignment as the forward. Workspace (16-byte aligned, at least
+ * moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, own_rows) bytes, PMN_EWORKSPACE; no initialization)
+ * holds wgrad's rows in slot order: own_rows is 1 with gather, or with x NULL, else 0 and nothing is needed.
+ */
+size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int own_rows);
+int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, const int32_t* gather, const void* w,
+                              const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, int flags,
+                              const void* h13, void* da, int da_dtype, void* db, int db_dtype, void* workspace,
+                              size_t workspace_bytes, pmn_stream_t stream);
+
+/*
+ * Products of a few tokens with NVFP4 weights and bf16 activations, for decoding (the rollouts of [AREX]'s
+ * title run the same 4-bit weights): T tokens, each with k of G experts,
+ *   y[t, j, n] = sum_k x(t, j)[k] w[ids[t, j]*N + n, k]
+ * w NVFP4 [G*N x K] (exact dequantized values, fp32 accumulation, the outer scale on the sum);
+ * x bf16 [T x K], or with x_per_pair [T*k x K], row t*k + j; ids int32 [T x k], or NULL with G == 1 and k == 1
+ * (a dense product). An id outside [0, G) gives zeros. The same id may stand in a token several times.
+ * gates NULL: epilogue PMN_EPI_F32 or _BF16, out [T*k x N]; PMN_EPI_SWIGLU (N = 2F, rows 0..F-1 of each
+ *   expert w1, F..2F-1 w3), out bf16 [T*k x F] = silu(h1) h3.
+ * gates fp32 [T x k]: out [T x N] = sum_j gates[t, j] y[t, j] + add[t] (add NULL, or bf16 [T x N]: the shared
+ *   expert's row), of fp32 (PMN_EPI_F32) or bf16; a pair whose id is outside [0, G) adds nothing.
+ * PMN_EINVAL: gates with SWIGLU, add without gates. N % 32 == 0 (SWIGLU: N % 64 == 0), K % 32 == 0, N and K <=
+ * 2^20, w_rows_per_outer % 32 == 0 (SWIGLU: F % w_rows_per_outer == 0 keeps w1 and w3 apart), T * k <= 4096
+ * (PMN_ESHAPE). x, w_codes, add and out 16-byte aligned, w_scales 4. Workspace (16-byte aligned, at least
+ * moe_gemv_nvfp4_workspace_size(T, k, N, gates != NULL) bytes, 0 for up to 16 tokens and 16 experts each;
+ * PMN_EWORKSPACE; no initialization) holds the pairs' rows in fp32.
+ */
+size_t moe_gemv_nvfp4_workspace_size(int64_t T, int k, int64_t N, int summed);
+int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const uint8_t* w_scales,
+                   const float* w_outer, int64_t w_rows_per_outer, const int32_t* ids, const float* gates,
+                   const void* add, int64_t T, int k, int G, int64_t N, int64_t K, int epilogue, void* out,
+                   void* workspace, size_t workspace_bytes, pmn_stream_t stream);
+
+/*
+ * The experts' unquantized rows y [M x H] of y_dtype (PMN_DTYPE_*) back to their T tokens:
+ *   out[t, :] = sum_j gates[t, j] y[slot_of[t, j], :] + add[t, :]
+ * slot_of int32 [T x k] (moe_route_topk's), or NULL: slot t*k + j (M >= T*k). gates fp32 [T x k], or NULL:
+ * ones (the sum of the slots' gradients of moe_grouped_gemm_bwd or _bwd_bf16). add: NULL, or bf16 [T x H]
+ * (it may be out itself where out is bf16). out [T x H] of out_dtype. Slots outside [0, M) are not read and
+ * add nothing. Sums are fp32 in the order of j. H % 8 == 0, H <= 2^20, 1 <= k <= 64, T < 2^24, M < 2^31
+ * (PMN_ESHAPE); y, add and out 16-byte aligned (PMN_EALIGN).
+ */
+int moe_combine_rows_fwd(const void* y, int y_dtype, int64_t M, int64_t H, const int32_t* slot_of, const float* gates,
+                         const void* add, int64_t T, int k, void* out, int out_dtype, pmn_stream_t stream);
+
+/*
+ * Its gradients from dout [T x H] of dout_dtype (the gradient of add is dout itself):
+ *   dy[slot_of[t, j], :] = gates[t, j] dout[t, :]     [M x H] of y_dtype, or NULL
+ *   dgates[t, j] = sum_h dout[t, h] y[slot_of[t, j], h]   fp32 [T x k], or NULL (then y may be NULL)
+ * Rows of dy that no pair names are left as they are; a pair whose slot is outside [0, M) writes no row and
+ * its dgates is zero. No slot may be named twice: its row of dy would be one pair's, not their sum. Sizes and
+ * alignment as the forward; dy and dgates not both NULL (PMN_EINVAL).
+ */
+int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype, int64_t M, int64_t H,
+                         const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy, float* dgates,
+                         pmn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Checking the device index contract (a debugging aid for callers; no other call runs it).   */
 /* ------------------------------------------------------------------------------------------ */
 

@@ -57,6 +57,13 @@ _SIGS = {
     "adamw_table_size": (SZ, [P, I32]),
     "adamw_table_build": (I32, [P, I32, I32, P, SZ, P]),
     "adamw_step": (I32, [P, I64, I32, F64, F64, F64, F64, I64, P, P, P, U64, U32, P]),
+    "moe_grouped_gemm_fwd_bf16": (I32, [P, I64, P, P, P, I32, I64, I64, I64, I32, P, P, P]),
+    "moe_grouped_gemm_bwd_bf16_workspace_size": (SZ, [I64, I64, I32, I32]),
+    "moe_grouped_gemm_bwd_bf16": (I32, [P, P, I64, P, P, P, I32, I64, I64, I64, I32, P, P, I32, P, I32, P, SZ, P]),
+    "moe_gemv_nvfp4_workspace_size": (SZ, [I64, I32, I64, I32]),
+    "moe_gemv_nvfp4": (I32, [P, I32, P, P, P, I64, P, P, P, I64, I32, I32, I64, I64, I32, P, P, SZ, P]),
+    "moe_combine_rows_fwd": (I32, [P, I32, I64, I64, P, P, P, I64, I32, P, I32, P]),
+    "moe_combine_rows_bwd": (I32, [P, I32, P, I32, I64, I64, P, P, I64, I32, P, P, P]),
     # measurement kernels (include/pmn_probe.h)
     "pmn_probe_stream": (I32, [P, P, I64, I32, I32, I32, I32, P]),
     "pmn_probe_mfma_sink_floats": (SZ, [I32, I32]),
@@ -796,6 +803,204 @@ def swiglu_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
         _device_ptr(dw2, at, "dw2"), DTYPE_F32 if dw_dtype == torch.float32 else DTYPE_BF16,
         _device_ptr(workspace, at, "workspace"), workspace.numel(), _raw_stream(at)), "swiglu_ffn_bwd")
     return dx, dw13, dw2
+
+
+# ---- the expert layer on unquantized activations --------------------------------------------
+
+def _group_args(w: torch.Tensor, offsets: torch.Tensor, M: int, N: int, gather, what: str, src_rows: int):
+    """(G, K) of bf16 weights [G*N, K]."""
+    _need(offsets is not None and offsets.dtype == torch.int64 and offsets.dim() == 1 and offsets.numel() >= 2,
+          "offsets must be int64 [G+1]")
+    G = offsets.numel() - 1
+    _need(w.dtype == torch.bfloat16 and w.dim() == 2 and w.shape[0] == G * N, f"w must be bf16 [G*N, K] with {G * N} rows")
+    _index(gather, M, torch.int32, "gather")
+    _debug_indices(what, offsets, M, gather, src_rows)
+    return G, w.shape[1]
+
+
+def moe_grouped_gemm_fwd_bf16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, M: int, N: int,
+                              epilogue: int = EPI_BF16, gather: Optional[torch.Tensor] = None, save_h13: bool = False,
+                              out: Optional[torch.Tensor] = None, out_aux: Optional[torch.Tensor] = None):
+    """Grouped product of bf16 x [rows, K] with bf16 w [G*N, K]: Y [M, N] (EPI_F32, EPI_BF16), or with
+    EPI_SWIGLU (silu(h1) * h3 [M, N/2], h1 | h3 [M, N] or None), as moe_grouped_gemm_fwd returns them."""
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [rows, K]")
+    _need(epilogue in (EPI_F32, EPI_BF16, EPI_SWIGLU), "epilogue must be EPI_F32, EPI_BF16 or EPI_SWIGLU")
+    G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_fwd_bf16", x.shape[0])
+    _need(x.shape[1] == K, f"x must have {K} columns")
+    at = _device_of(w, "w")
+    dev = w.device
+    swiglu = epilogue == EPI_SWIGLU
+    if out is None:
+        out = torch.empty((M, N // 2 if swiglu else N), dtype=torch.float32 if epilogue == EPI_F32 else torch.bfloat16,
+                          device=dev)
+    if swiglu and save_h13 and out_aux is None:
+        out_aux = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _epilogue_outputs(epilogue, M, N, out, None, out_aux)
+    _check(_lib.moe_grouped_gemm_fwd_bf16(
+        _device_ptr(x, at, "x"), x.shape[0], _device_ptr(gather, at, "gather"), _device_ptr(w, at, "w"),
+        _device_ptr(offsets, at, "offsets"), G, M, N, K, epilogue, _device_ptr(out, at, "out"),
+        _device_ptr(out_aux, at, "out_aux") if swiglu else None, _raw_stream(at)), "moe_grouped_gemm_fwd_bf16")
+    return (out, out_aux) if swiglu else out
+
+
+def moe_grouped_gemm_bwd_bf16_workspace_size(M: int, K: int, flags: int, own_rows: bool) -> int:
+    return _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(own_rows))
+
+
+def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor, offsets: torch.Tensor,
+                              M: int, N: int, flags: int = BWD_DGRAD | BWD_WGRAD,
+                              gather: Optional[torch.Tensor] = None, h13: Optional[torch.Tensor] = None,
+                              da_dtype: torch.dtype = torch.bfloat16, db_dtype: torch.dtype = torch.float32,
+                              workspace: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
+                              db: Optional[torch.Tensor] = None):
+    """Backward of moe_grouped_gemm_fwd_bf16. Returns (da [M, K] or None, db [G*N, K] or None), as flags asks.
+    h13 [M, 2K]: the gradient goes on through the SwiGLU that made the product's input, and da is dh13
+    [M, 2K]; x may then be None (its values are taken from h13)."""
+    _tensor(dy, (M, N), torch.bfloat16, "dy")
+    dgrad, wgrad = bool(flags & BWD_DGRAD), bool(flags & BWD_WGRAD)
+    for name, dt in (("da_dtype", da_dtype), ("db_dtype", db_dtype)):
+        _need(dt in (torch.bfloat16, torch.float32), f"{name} must be bf16 or fp32")
+    _need(dgrad or da is None, "da needs BWD_DGRAD")
+    _need(wgrad or db is None, "db needs BWD_WGRAD")
+    _need(x is not None or not wgrad or h13 is not None, "the weight gradient needs x or h13")
+    G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_bwd_bf16", 0 if x is None else x.shape[0])
+    if x is not None:
+        _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == K, f"x must be bf16 [rows, {K}]")
+    if h13 is not None:
+        _tensor(h13, (M, 2 * K), torch.bfloat16, "h13")
+        _need(gather is None and dgrad and da_dtype == torch.bfloat16, "h13 goes with BWD_DGRAD, a bf16 da and no gather")
+    at = _device_of(dy, "dy")
+    dev = dy.device
+    width = K if h13 is None else 2 * K
+    if da is not None:
+        _tensor(da, (M, width), da_dtype, "da")
+    elif dgrad:
+        da = torch.empty((M, width), dtype=da_dtype, device=dev)
+    if db is not None:
+        _tensor(db, (G * N, K), db_dtype, "db")
+    elif wgrad:
+        db = torch.empty((G * N, K), dtype=db_dtype, device=dev)
+    need = _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(gather is not None or x is None))
+    workspace = _workspace(workspace, need, dev) if need or workspace is not None else None
+    _check(_lib.moe_grouped_gemm_bwd_bf16(
+        _device_ptr(dy, at, "dy"), _device_ptr(x, at, "x"), 0 if x is None else x.shape[0],
+        _device_ptr(gather, at, "gather"), _device_ptr(w, at, "w"), _device_ptr(offsets, at, "offsets"), G, M, N, K, flags,
+        _device_ptr(h13, at, "h13"), _device_ptr(da, at, "da"), DTYPE_F32 if da_dtype == torch.float32 else DTYPE_BF16,
+        _device_ptr(db, at, "db"), DTYPE_F32 if db_dtype == torch.float32 else DTYPE_BF16,
+        _device_ptr(workspace, at, "workspace"), 0 if workspace is None else workspace.numel(), _raw_stream(at)),
+        "moe_grouped_gemm_bwd_bf16")
+    return da, db
+
+
+def moe_gemv_nvfp4_workspace_size(T: int, k: int, N: int, summed: bool) -> int:
+    return _lib.moe_gemv_nvfp4_workspace_size(T, k, N, int(summed))
+
+
+def moe_gemv_nvfp4(x: torch.Tensor, wq: NVFP4, N: int, ids: Optional[torch.Tensor] = None, epilogue: int = EPI_BF16,
+                   gates: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A few tokens' bf16 activations times NVFP4 weights wq [G*N, K]. x [T, K], or [T, k, K] with a row for
+    each of a token's experts; ids int32 [T, k] names them (None: G = 1, a dense product). Without gates
+    y [T, k, N] (without ids [T, N]) in fp32 or bf16, or with EPI_SWIGLU silu(h1) * h3 [T, k, N/2] in bf16; with
+    gates fp32 [T, k] their sum over k (+ add bf16 [T, N]), [T, N]."""
+    _need(x.dtype == torch.bfloat16 and x.dim() in (2, 3), "x must be bf16 [T, K] or [T, k, K]")
+    _need(epilogue in (EPI_F32, EPI_BF16, EPI_SWIGLU), "epilogue must be EPI_F32, EPI_BF16 or EPI_SWIGLU")
+    _nvfp4(wq, "wq")
+    T, K = x.shape[0], x.shape[-1]
+    _need(wq.cols == K, f"wq must have {K} columns")
+    _need(N > 0 and wq.rows % N == 0 and wq.rows > 0, f"wq must have a multiple of {N} rows")
+    G, k = wq.rows // N, 1
+    if ids is not None:
+        _need(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == T, f"ids must be int32 [{T}, k]")
+        k = ids.shape[1]
+    else:
+        _need(G == 1, f"without ids wq must have {N} rows")
+    _need(x.dim() == 2 or x.shape[1] == k, f"x must have {k} rows a token")
+    if gates is not None:
+        _tensor(gates, (T, k), torch.float32, "gates")
+        _need(epilogue != EPI_SWIGLU, "gates do not go with EPI_SWIGLU")
+    if add is not None:
+        _need(gates is not None, "add needs gates")
+        _tensor(add, (T, N), torch.bfloat16, "add")
+    at = _device_of(x, "x")
+    dev = x.device
+    width = N // 2 if epilogue == EPI_SWIGLU else N
+    shape = (T, width) if gates is not None or ids is None else (T, k, width)
+    dtype = torch.float32 if epilogue == EPI_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    _tensor(out, shape, dtype, "out")
+    if gates is not None:
+        need = _lib.moe_gemv_nvfp4_workspace_size(T, k, N, 1)
+        workspace = _workspace(workspace, need, dev) if need or workspace is not None else None
+    _check(_lib.moe_gemv_nvfp4(
+        _device_ptr(x, at, "x"), int(x.dim() == 3), _device_ptr(wq.codes, at, "wq.codes"),
+        _device_ptr(wq.scales, at, "wq.scales"), _device_ptr(wq.outer, at, "wq.outer"), wq.rows_per_outer,
+        _device_ptr(ids, at, "ids"), _device_ptr(gates, at, "gates"), _device_ptr(add, at, "add"), T, k, G, N, K, epilogue,
+        _device_ptr(out, at, "out"), _device_ptr(workspace, at, "workspace"),
+        0 if workspace is None else workspace.numel(), _raw_stream(at)), "moe_gemv_nvfp4")
+    return out
+
+
+def _rows_args(y: torch.Tensor, slot_of: torch.Tensor, gates: Optional[torch.Tensor]):
+    """(M, H, T, k) of y [M, H] and slot_of [T, k], or [T*k] as moe_route_topk gives it, beside gates [T, k]."""
+    _need(y.dim() == 2, "y must be [M, H]")
+    shape = slot_of.shape
+    if slot_of.dim() == 1 and gates is not None and gates.dim() == 2:
+        shape = gates.shape
+    _need(slot_of.dtype == torch.int32 and len(shape) == 2 and slot_of.numel() == shape[0] * shape[1],
+          "slot_of must be int32 [T, k] (or [T*k] with gates)")
+    if gates is not None:
+        _tensor(gates, shape, torch.float32, "gates")
+    return (*y.shape, *shape)
+
+
+def moe_combine_rows_fwd(y: torch.Tensor, slot_of: torch.Tensor, gates: Optional[torch.Tensor] = None,
+                         add: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Row t = sum_j gates[t, j] * y[slot_of[t, j]] (+ add[t]): y bf16 or fp32 [M, H], gates None: ones, add
+    bf16 [T, H] (it may be out). A slot outside [0, M) adds nothing."""
+    ycode = _dtype_code(y, "y")
+    M, H, T, k = _rows_args(y, slot_of, gates)
+    if add is not None:
+        _tensor(add, (T, H), torch.bfloat16, "add")
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bf16 or fp32")
+    at = _device_of(slot_of, "slot_of")
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=y.device)
+    _tensor(out, (T, H), out_dtype, "out")
+    _check(_lib.moe_combine_rows_fwd(
+        _device_ptr(y, at, "y"), ycode, M, H, _device_ptr(slot_of, at, "slot_of"), _device_ptr(gates, at, "gates"),
+        _device_ptr(add, at, "add"), T, k, _device_ptr(out, at, "out"),
+        DTYPE_F32 if out_dtype == torch.float32 else DTYPE_BF16, _raw_stream(at)), "moe_combine_rows_fwd")
+    return out
+
+
+def moe_combine_rows_bwd(dout: torch.Tensor, y: torch.Tensor, slot_of: torch.Tensor,
+                         gates: Optional[torch.Tensor] = None, want_dy: bool = True, want_dgates: bool = True,
+                         dy: Optional[torch.Tensor] = None):
+    """Gradients of moe_combine_rows_fwd from dout [T, H] (bf16 or fp32): (dy [M, H] of y's type or None, dgates
+    fp32 [T, k] or None). No slot may be named twice. Rows of a given dy that no pair names are left as they
+    are; without one they are zeros, but with M == T * k every slot has to be named."""
+    ycode, dcode = _dtype_code(y, "y"), _dtype_code(dout, "dout")
+    M, H, T, k = _rows_args(y, slot_of, gates)
+    _tensor(dout, (T, H), dout.dtype, "dout")
+    _need(want_dy or dy is None, "dy needs want_dy")
+    _need(want_dy or want_dgates, "want_dy or want_dgates must be set")
+    if dy is not None:
+        _tensor(dy, (M, H), y.dtype, "dy")
+    at = _device_of(slot_of, "slot_of")
+    if CHECK_INDICES and want_dy:
+        inside = slot_of[(slot_of >= 0) & (slot_of < M)]
+        _need(inside.unique().numel() == inside.numel(), "moe_combine_rows_bwd: a slot is named twice")
+    if want_dy and dy is None:
+        dy = torch.empty_like(y) if M == T * k else torch.zeros_like(y)
+    dgates = torch.empty((T, k), dtype=torch.float32, device=y.device) if want_dgates else None
+    _check(_lib.moe_combine_rows_bwd(
+        _device_ptr(dout, at, "dout"), dcode, _device_ptr(y, at, "y"), ycode, M, H, _device_ptr(slot_of, at, "slot_of"),
+        _device_ptr(gates, at, "gates"), T, k, _device_ptr(dy, at, "dy"), _device_ptr(dgates, at, "dgates"),
+        _raw_stream(at)), "moe_combine_rows_bwd")
+    return dy, dgates
 
 
 @dataclass

@@ -574,6 +574,149 @@ int swiglu_ffn_bwd(const void* dy, const void* x, const void* w13, const void* w
         wgrad ? dw13 : nullptr, dw2, dw_dtype == PMN_DTYPE_F32, hs(stream)));
 }
 
+static bool bad_group_shape(int64_t M, int G, int64_t N, int64_t K, int64_t x_rows, bool gathered)
+{
+    const int64_t most = (int64_t)1 << 20;
+    return G < 1 || M < 0 || M >= ((int64_t)1 << 31) || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || N > most ||
+           K > most || x_rows < 0 || (!gathered && M > x_rows);
+}
+
+int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gather, const void* w,
+                              const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out,
+                              void* out_aux, pmn_stream_t stream)
+{
+    if (epilogue != PMN_EPI_F32 && epilogue != PMN_EPI_BF16 && epilogue != PMN_EPI_SWIGLU) return PMN_EINVAL;
+    if (bad_group_shape(M, G, N, K, x_rows, gather != nullptr) || (epilogue == PMN_EPI_SWIGLU && N % 16 != 0) ||
+        !pmn::group_bf16_fits(M, G, N, K, true))
+        return PMN_ESHAPE;
+    if (M == 0) return PMN_OK;
+    if (!x || !w || !offsets || !out) return PMN_EINVAL;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(out_aux, 16) || !aligned(gather, 4) ||
+        !aligned(offsets, 8))
+        return PMN_EALIGN;
+    return status(pmn::launch_group_fwd_bf16(static_cast<const uint16_t*>(x), gather, static_cast<const uint16_t*>(w),
+                                             offsets, G, M, N, K, epilogue, out, static_cast<uint16_t*>(out_aux),
+                                             hs(stream)));
+}
+
+size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int own_rows)
+{
+    return M <= 0 || K <= 0 || !(flags & PMN_BWD_WGRAD) || !own_rows ? 0 : round256((size_t)(M * K) * 2);
+}
+
+int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, const int32_t* gather, const void* w,
+                              const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, int flags,
+                              const void* h13, void* da, int da_dtype, void* db, int db_dtype, void* workspace,
+                              size_t workspace_bytes, pmn_stream_t stream)
+{
+    if ((flags & ~(PMN_BWD_DGRAD | PMN_BWD_WGRAD)) != 0 || flags == 0) return PMN_EINVAL;
+    const bool dgrad = flags & PMN_BWD_DGRAD, wgrad = flags & PMN_BWD_WGRAD;
+    if ((dgrad && (bad_dtype(da_dtype) || (h13 && da_dtype != PMN_DTYPE_BF16))) || (wgrad && bad_dtype(db_dtype)) ||
+        (h13 && (gather || !dgrad)))
+        return PMN_EINVAL;
+    if (bad_group_shape(M, G, N, K, wgrad && x ? x_rows : M, gather != nullptr) ||
+        !pmn::group_bf16_fits(M, G, N, K, false))
+        return PMN_ESHAPE;
+    const bool rebuild = wgrad && !x && h13;
+    if (!offsets || (wgrad && !db)) return PMN_EINVAL;
+    if (M > 0 && (!dy || (dgrad && (!w || !da)) || (wgrad && !x && !rebuild))) return PMN_EINVAL;
+    const size_t need = moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, gather != nullptr || rebuild);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PMN_EWORKSPACE;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(h13, 16) || !aligned(gather, 4) ||
+        !aligned(offsets, 8) || (dgrad && !aligned(da, 16)) || (wgrad && !aligned(db, 16)) ||
+        (need > 0 && !aligned(workspace, 16)))
+        return PMN_EALIGN;
+    if (M == 0 && !wgrad) return PMN_OK;
+    uint16_t* const rows = need > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
+    return status(pmn::launch_group_bwd_bf16(
+        static_cast<const uint16_t*>(dy), rebuild ? rows : static_cast<const uint16_t*>(x), gather,
+        static_cast<const uint16_t*>(w), offsets, G, M, N, K, static_cast<const uint16_t*>(h13), dgrad ? da : nullptr,
+        da_dtype == PMN_DTYPE_F32, rebuild ? rows : nullptr, rows, wgrad ? db : nullptr, db_dtype == PMN_DTYPE_F32,
+        hs(stream)));
+}
+
+static bool bad_gemv_shape(int64_t T, int k, int G, int64_t N, int64_t K)
+{
+    return T < 0 || k < 1 || G < 1 || N <= 0 || K <= 0 || N % 32 != 0 || K % 32 != 0 || N > ((int64_t)1 << 20) ||
+           K > ((int64_t)1 << 20) || T > pmn::gemv_most_pairs() || T * k > pmn::gemv_most_pairs();
+}
+
+size_t moe_gemv_nvfp4_workspace_size(int64_t T, int k, int64_t N, int summed)
+{
+    if (!summed || T <= 0 || k < 1 || N <= 0 || T > pmn::gemv_most_pairs() || pmn::gemv_sums_at_once((int)T, k)) return 0;
+    return round256((size_t)(T * k * N) * 4);
+}
+
+int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const uint8_t* w_scales,
+                   const float* w_outer, int64_t w_rows_per_outer, const int32_t* ids, const float* gates,
+                   const void* add, int64_t T, int k, int G, int64_t N, int64_t K, int epilogue, void* out,
+                   void* workspace, size_t workspace_bytes, pmn_stream_t stream)
+{
+    if (epilogue != PMN_EPI_F32 && epilogue != PMN_EPI_BF16 && epilogue != PMN_EPI_SWIGLU) return PMN_EINVAL;
+    if ((gates && epilogue == PMN_EPI_SWIGLU) || (add && !gates)) return PMN_EINVAL;
+    if (bad_gemv_shape(T, k, G, N, K) || w_rows_per_outer < 32 || w_rows_per_outer % 32 != 0) return PMN_ESHAPE;
+    if (epilogue == PMN_EPI_SWIGLU && N % 64 != 0) return PMN_ESHAPE;
+    if (!ids && (G != 1 || k != 1)) return PMN_EINVAL;
+    // workgroups of 512 threads, one for 8 or 16 rows: a launch has fewer than 2^32 threads
+    const int64_t experts = ids ? (T * k < G ? T * k : G) : 1;
+    if (experts * (N / 16) >= ((int64_t)1 << 23)) return PMN_ESHAPE;
+    if (T == 0) return PMN_OK;
+    if (!x || !w_codes || !w_scales || !w_outer || !out) return PMN_EINVAL;
+    const size_t need = moe_gemv_nvfp4_workspace_size(T, k, N, gates != nullptr);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PMN_EWORKSPACE;
+    if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(w_outer, 4) || !aligned(ids, 4) ||
+        !aligned(gates, 4) || !aligned(add, 16) || !aligned(out, 16) || (need > 0 && !aligned(workspace, 16)))
+        return PMN_EALIGN;
+    const uint16_t* xs = static_cast<const uint16_t*>(x);
+    const uint16_t* as = static_cast<const uint16_t*>(add);
+    if (!gates)
+        return status(pmn::launch_gemv_pairs(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids, (int)T,
+                                             k, G, N, K, epilogue, out, hs(stream)));
+    const bool f32 = epilogue == PMN_EPI_F32;
+    if (need == 0)
+        return status(pmn::launch_gemv_sum(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids, gates,
+                                           as, (int)T, k, G, N, K, f32, out, hs(stream)));
+    const hipError_t e = pmn::launch_gemv_pairs(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids,
+                                                (int)T, k, G, N, K, PMN_EPI_F32, workspace, hs(stream));
+    if (e != hipSuccess) return PMN_ELAUNCH;
+    return status(pmn::launch_combine_rows(workspace, true, T * k, N, nullptr, gates, as, T, k, out, f32, hs(stream)));
+}
+
+static bool bad_rows_shape(int64_t M, int64_t H, int64_t T, int k)
+{
+    return M < 0 || M >= ((int64_t)1 << 31) || H < 0 || H % 8 != 0 || H > ((int64_t)1 << 20) || T < 0 ||
+           T >= ((int64_t)1 << 24) || k < 1 || k > 64;
+}
+
+int moe_combine_rows_fwd(const void* y, int y_dtype, int64_t M, int64_t H, const int32_t* slot_of, const float* gates,
+                         const void* add, int64_t T, int k, void* out, int out_dtype, pmn_stream_t stream)
+{
+    if (bad_dtype(y_dtype) || bad_dtype(out_dtype)) return PMN_EINVAL;
+    if (bad_rows_shape(M, H, T, k) || (!slot_of && M < T * k)) return PMN_ESHAPE;
+    if (T == 0 || H == 0) return PMN_OK;
+    if (!out || (M > 0 && !y)) return PMN_EINVAL;
+    if (!aligned(y, 16) || !aligned(add, 16) || !aligned(out, 16) || !aligned(slot_of, 4) || !aligned(gates, 4)) return PMN_EALIGN;
+    return status(pmn::launch_combine_rows(y, y_dtype == PMN_DTYPE_F32, M, H, slot_of, gates,
+                                           static_cast<const uint16_t*>(add), T, k, out, out_dtype == PMN_DTYPE_F32,
+                                           hs(stream)));
+}
+
+int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype, int64_t M, int64_t H,
+                         const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy, float* dgates,
+                         pmn_stream_t stream)
+{
+    if (bad_dtype(dout_dtype) || bad_dtype(y_dtype)) return PMN_EINVAL;
+    if (bad_rows_shape(M, H, T, k) || (!slot_of && M < T * k)) return PMN_ESHAPE;
+    if (!dy && !dgates) return PMN_EINVAL;
+    if (T == 0) return PMN_OK;
+    if (H > 0 && (!dout || (dgates && M > 0 && !y))) return PMN_EINVAL;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(dgates, 4) || !aligned(slot_of, 4) ||
+        !aligned(gates, 4))
+        return PMN_EALIGN;
+    return status(pmn::launch_combine_rows_bwd(dout, dout_dtype == PMN_DTYPE_F32, y, y_dtype == PMN_DTYPE_F32, M, H,
+                                               slot_of, gates, T, k, dy, dgates, hs(stream)));
+}
+
 // a chunk has 256 threads, and a launch fewer than 2^32
 constexpr int64_t ADAMW_MOST_CHUNKS = (int64_t)1 << 24;
 static int64_t adamw_chunks_of(int64_t n) { return n <= 0 ? 0 : (n + pmn::adamw_chunk() - 1) / pmn::adamw_chunk(); }

@@ -43,12 +43,13 @@ struct FfnArgs {
     int64_t Nr, Nc, K;      // product: Nc output rows x Nr output columns, contraction K
     void* out;              // [Nc x Nr] (SWIGLU: a [Nc x F]; SWIGLU_BWD: dh13 [Nc x 2F])
     const uint16_t* aux;    // ADD: add (or null); SWIGLU_BWD: h13
-    uint16_t* out2;         // SWIGLU: h13 (or null); SWIGLU_BWD: a
+    uint16_t* out2;         // SWIGLU: h13 (or null); SWIGLU_BWD: a (or null)
     int64_t F;
     float* part;            // PART: [splits x Nc x Nr]
     int splits;
     int64_t rtiles, ctiles;
     int64_t whole;          // tiles that run whole; the others in two halves (ffn_grid)
+    const int32_t* gather;  // GATHER: the stored row of C that each of its rows is
 };
 
 // The 16-byte words of aux that 8 consecutive outputs n .. n+7 of output row c need: ADD's add, or
@@ -111,7 +112,7 @@ PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], 
         }
         put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + n, v, false);
         put(static_cast<uint16_t*>(p.out) + c * 2 * p.F + p.F + n, v2, false);
-        put(p.out2 + c * p.F + n, a, false);
+        if (p.out2) put(p.out2 + c * p.F + n, a, false);
     } else if (EPI == FFN_F32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + c * p.Nr + n);
         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -145,6 +146,13 @@ PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
 }
 
 constexpr uint32_t FFN_OUTSIDE = 0x80000000u;   // a buffer offset past every descriptor
+
+// The same from an address of the lane's own: rows that are gathered lie anywhere in 64 bits.
+PMN_DEV void dma16_flat(const void* src, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+static __device__ const uint4 ffn_zeros = {0u, 0u, 0u, 0u};   // what a gathered chunk outside the operand reads
 
 // WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of 5 filled in pairs
 template <int WR_, int WC_, int RB_, int CB_, int NST_>
@@ -183,14 +191,16 @@ PMN_DEV void ffn_tile_at(const FfnArgs& p, int64_t i, int64_t& trow, int64_t& tc
     trow = band * 8 + (in - tcol * height);
 }
 
-// The tile (trow, tcol) of a product, or part `split` of its contraction (PART).
-template <typename T, bool RKC, bool CKC, int EPI>
+// The tile (trow, tcol) of a product, or part `split` of its contraction (PART). GATHER: row i of C
+// (k-contiguous) is stored row gather[i] of c.
+template <typename T, bool RKC, bool CKC, int EPI, bool GATHER = false>
 PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, uint8_t* lds)
 {
     constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, PPW = T::PPW;
     constexpr bool SWI = EPI == FFN_SWIGLU, PAIRED = T::PAIRS && RKC && CKC;
     constexpr int NST = PAIRED ? 5 : T::NST;
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
+    static_assert(!GATHER || CKC, "rows are gathered of a k-contiguous operand");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / T::WC, wc = wave % T::WC, l32 = lane & 31, hh = lane >> 5;
@@ -212,6 +222,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     };
     uint32_t voff[PPW];
     int kch[PPW];
+    const uint8_t* from[GATHER ? T::CPW : 1];   // the gathered rows' chunks at this part's first stage
 #pragma unroll
     for (int i = 0; i < PPW; i++) {
         const bool isr = i < T::RPW;
@@ -231,6 +242,11 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             }
             voff[i] = ok ? (uint32_t)(row * ld * 2 + ch * 16) : FFN_OUTSIDE;
             kch[i] = ch * 8;
+            if (GATHER && !isr) {
+                from[i - T::RPW] = ok ? reinterpret_cast<const uint8_t*>(p.c + (int64_t)p.gather[c0 + t] * ld + s0 * 32 + ch * 8)
+                                      : nullptr;
+                if (!ok) kch[i] = 32;   // past every stage
+            }
         } else {
             const int W = isr ? BR * 2 : BC * 2;                      // bytes of a stored row in the tile
             const int k = (q * 1024 + lane * 16) / W, ch = (q * 1024 + lane * 16) % W / 16;
@@ -262,7 +278,8 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     const int64_t w3_bytes = SWI ? p.F * p.ldr * 2 : 0;
     struct Stage {
         i32x4 r, r3, c;   // r3: the rows of w3
-        int left;         // k of this stage, at most 32
+        int left;         // k of this stage, at most 32; nothing is gathered past the part's last stage
+        int64_t at;       // its bytes from the part's first (GATHER)
         uint32_t dst;
     };
     auto stage_at = [&](int s) {
@@ -270,8 +287,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         const bool in = s < nst;   // nothing past the part's last stage
         g.r = buffer_of(opr.base + s * opr.step, in ? opr.bytes - s * opr.step : 0);
         if (SWI) g.r3 = buffer_of(opr.base + w3_bytes + s * opr.step, in ? opr.bytes - s * opr.step : 0);
-        g.c = buffer_of(opc.base + s * opc.step, in ? opc.bytes - s * opc.step : 0);
-        const int64_t left = p.K - (s0 + s) * 32;
+        if (!GATHER) g.c = buffer_of(opc.base + s * opc.step, in ? opc.bytes - s * opc.step : 0);
+        g.at = (int64_t)s * 64;
+        const int64_t left = GATHER && !in ? 0 : p.K - (s0 + s) * 32;
         g.left = left > 32 ? 32 : (int)left;
         g.dst = (uint32_t)(s % NST) * T::STAGE;
         return g;
@@ -280,7 +298,10 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         const bool isr = i < T::RPW;
         // chunks past K of a k-contiguous operand
         const uint32_t v = (isr ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i];
-        if (!isr) {
+        if (GATHER && !isr) {
+            const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
+            dma16_flat(kch[i] >= g.left ? z : from[i - T::RPW] + g.at, g.dst + lds0 + T::RBYTES + piece_of(i) * 1024);
+        } else if (!isr) {
             dma16_buffer(g.c, v, g.dst + lds0 + T::RBYTES + piece_of(i) * 1024);
         } else if (!SWI) {
             dma16_buffer(g.r, v, g.dst + lds0 + piece_of(i) * 1024);

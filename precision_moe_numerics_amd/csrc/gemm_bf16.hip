@@ -1,0 +1,334 @@
+// gemm_bf16.hip -- bf16 products grouped by expert, for layers (or passes) that are not quantized:
+//     forward  Y[s, n] = sum_k x[row_s, k] W_g[n, k]        (bf16, fp32, or SwiGLU with h1 | h3 saved)
+//     dgrad    da[s, k] = sum_n dY[s, n] W_g[n, k]          (or on through the SwiGLU: dh13)
+//     wgrad    dW_g[n, k] = sum_{s in g} dY[s, n] x[row_s, k]
+// g the group of slot s, row_s = gather[s] or s. Group sizes are on the device only.
+//
+// The tiles are bf16_tile.hpp's. Forward and dgrad run over the concatenation of the groups' units of
+// BC slots; a workgroup finds its unit with one wavefront-parallel search of the offsets, and a unit of
+// at most BC / 2 slots that ends a group runs as half a tile. Wgrad runs over the groups' (n, k) tiles,
+// each of its group's length; a group without slots writes zeros.
+//
+// Sums are fp32; outputs are rounded once.
+#include "bf16_tile.hpp"
+#include "pmn_kernels.hpp"
+
+namespace pmn {
+
+struct GroupArgs {
+    FfnArgs p;                // of the whole matrices; a workgroup moves the pointers to its group
+    const int64_t* offsets;
+    int G;
+    int64_t rgroup;           // elements of R between groups' matrices
+    int64_t out_width;        // output elements of a slot, and bytes of each
+    int out_bytes;
+    int64_t out2_width;
+};
+
+// Moves p to group g, whose slots are s0 .. s1
+template <bool GATHER>
+PMN_DEV void group_at(const GroupArgs& a, int g, int64_t s0, int64_t s1, FfnArgs& p)
+{
+    p = a.p;
+    p.r += g * a.rgroup;
+    if (GATHER) p.gather += s0;
+    else p.c += s0 * p.ldc;
+    p.Nc = s1 - s0;
+    p.out = static_cast<uint8_t*>(p.out) + s0 * a.out_width * a.out_bytes;
+    if (p.out2) p.out2 += s0 * a.out2_width;
+    if (p.aux) p.aux += s0 * 2 * p.F;
+}
+
+// Units of `unit` slots over all groups, on the device.
+PMN_DEV int64_t group_units(const int64_t* offsets, int G, int64_t unit)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t n = 0;
+    for (int g = lane; g < G; g += 64) n += (offsets[g + 1] - offsets[g] + unit - 1) / unit;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, 64);
+    return n;
+}
+
+PMN_DEV int64_t uniform64(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Workgroup L's tile of a product over the groups' slots: units of `unit` slots, a.p.rtiles tiles
+// of R each. Consecutive tiles of a group run on one XCD in bands of 8 tiles of R, so that they share
+// panels of both operands in its L2. False past the last.
+template <bool GATHER>
+PMN_DEV bool group_tile(const GroupArgs& a, int64_t L, int64_t unit, FfnArgs& p, int64_t& trow, int64_t& tcol)
+{
+    const int64_t i = ffn_item_of(uniform64(group_units(a.offsets, a.G, unit)) * a.p.rtiles, L);
+    if (i < 0) return false;
+    const int64_t u = i / a.p.rtiles;
+    const GroupUnit w = locate_group_unit(a.offsets, a.G, u, unit);
+    if (w.g < 0) return false;
+    const int64_t s0 = uniform64(w.s0), s1 = uniform64(w.s1), first = u - uniform64(w.index);
+    group_at<GATHER>(a, __builtin_amdgcn_readfirstlane(w.g), s0, s1, p);
+    p.ctiles = (s1 - s0 + unit - 1) / unit;
+    ffn_tile_at(p, i - first * a.p.rtiles, trow, tcol);
+    return true;
+}
+
+template <typename T, bool RKC, int EPI, bool GATHER>
+__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_group_gemm(GroupArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+    if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));   // keeps the 256 accumulators in AGPRs
+    FfnArgs p;
+    int64_t trow, tcol;
+    if (!group_tile<GATHER>(a, blockIdx.x, T::BC, p, trow, tcol)) return;
+    if constexpr (T::HALVES) {
+        if (p.Nc - tcol * T::BC <= T::BC / 2) {
+            ffn_tile<typename T::Half, RKC, true, EPI, GATHER>(p, trow, 2 * tcol, 0, lds);
+            return;
+        }
+    }
+    ffn_tile<T, RKC, true, EPI, GATHER>(p, trow, tcol, 0, lds);
+}
+
+// dW: p.Nr = K columns, p.Nc = N rows, contraction over the group's slots. The tiles of each group are
+// dealt to all XCDs in runs, as the groups differ in length.
+template <typename T, int EPI>
+__global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_group_wgrad(GroupArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+    if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));
+    const int64_t tiles = a.p.rtiles * a.p.ctiles, per = (tiles + 7) >> 3;
+    const int64_t j = blockIdx.x >> 3, g = j / per, i = (blockIdx.x & 7) * per + (j - g * per);
+    if (i >= tiles || g >= a.G) return;
+    const int64_t s0 = uniform64(a.offsets[g]), s1 = uniform64(a.offsets[g + 1]);
+    FfnArgs p = a.p;
+    p.r += s0 * p.ldr;
+    p.c += s0 * p.ldc;
+    p.K = s1 - s0;
+    p.out = static_cast<uint8_t*>(p.out) + g * p.Nc * p.Nr * a.out_bytes;
+    int64_t trow, tcol;
+    ffn_tile_at(p, i, trow, tcol);
+    ffn_tile<T, false, false, EPI>(p, trow, tcol, 0, lds);
+}
+
+// Forward for few slots a group: units of 16 slots, the weights straight to registers. A workgroup holds
+// 16 rows of W_g (SWIGLU: 8 features of w1 and the same of w3); its 8 wavefronts share the contraction
+// in units of 64 k, one 128-byte line of each row, dealt in turn so that together they walk the rows, and
+// their sums are added in order through LDS. Lanes past the unit's last slot repeat it and store nothing.
+template <int EPI, bool GATHER>
+__global__ __launch_bounds__(512, 2) void k_group_few(GroupArgs a)
+{
+    constexpr bool SWI = EPI == FFN_SWIGLU;
+    constexpr int W = 8, U = 4;
+    __shared__ float4 red[W][64];
+    FfnArgs p;
+    int64_t trow, tcol;
+    if (!group_tile<GATHER>(a, blockIdx.x, 16, p, trow, tcol)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    const int64_t r0 = trow * (SWI ? 8 : 16), c = tcol * 16 + l16;
+    const int64_t rows = SWI ? p.F : p.Nr;
+    int64_t row = SWI ? r0 + (l16 & 7) : r0 + l16;
+    row = row < rows ? row : rows - 1;
+    if (SWI && l16 >= 8) row += p.F;
+    const uint16_t* const rp = p.r + row * p.ldr + 8 * g;
+    const int64_t slot = c < p.Nc ? c : p.Nc - 1;
+    const uint16_t* const cp = p.c + (GATHER ? (int64_t)p.gather[slot] : slot) * p.ldc + 8 * g;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t units = p.K >> 6;
+    auto load = [](const uint16_t* q) { return *reinterpret_cast<const bf16x8*>(q); };
+    auto batch = [&](int64_t u, auto checked) {
+        bf16x8 r[U][2], x[U][2];
+#pragma unroll
+        for (int i = 0; i < U; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t k = (u + W * i) * 64 + 32 * h;
+                if (!decltype(checked)::value || k + 8 * g < p.K) {
+                    r[i][h] = load(rp + k);
+                    x[i][h] = load(cp + k);
+                } else {
+                    r[i][h] = bf16x8{};
+                    x[i][h] = bf16x8{};
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < U; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r[i][h], x[i][h], acc, 0, 0, 0);
+    };
+    int64_t u = wave;
+    for (; u + W * (U - 1) < units; u += W * U) batch(u, std::false_type{});
+    for (; u * 64 < p.K; u += W * U) batch(u, std::true_type{});
+    red[wave][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (wave > 0) return;
+    // lane l finishes rows 4 (l / 16) .. +3 of column l % 16
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+        const float4 s = red[w][lane];
+        v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
+    }
+    auto put = [](uint16_t* dst, const float (&o)[4]) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
+    };
+    if (SWI) {
+        // lanes 0 .. 31 hold h1 of 8 features, lanes 32 .. 63 their h3
+        float h3[4], o[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            h3[i] = __shfl_xor(v[i], 32, 64);
+            o[i] = silu(v[i]) * h3[i];
+        }
+        const int64_t f = r0 + 4 * g;
+        if (g >= 2 || c >= p.Nc || f >= p.F) return;
+        put(static_cast<uint16_t*>(p.out) + c * p.F + f, o);
+        if (p.out2) {
+            put(p.out2 + c * 2 * p.F + f, v);
+            put(p.out2 + c * 2 * p.F + p.F + f, h3);
+        }
+    } else {
+        const int64_t n = r0 + 4 * g;
+        if (c >= p.Nc || n >= p.Nr) return;
+        if (EPI == FFN_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + c * p.Nr + n) = make_float4(v[0], v[1], v[2], v[3]);
+        else put(static_cast<uint16_t*>(p.out) + c * p.Nr + n, v);
+    }
+}
+
+typedef FfnTile<2, 2, 4, 4, 4> GroupLarge;   // 256 x 256, one workgroup per CU
+typedef FfnTile<2, 2, 2, 2, 4> GroupMid;     // 128 x 128
+typedef FfnTile<2, 2, 2, 1, 4> GroupSlim;    // 128 x 64
+
+// Tile by the mean slots of a group: 0 large, 1 mid, 2 slim, 3 sixteen slots (k-contiguous weights)
+static int group_plan(int64_t M, int G, bool rkc)
+{
+    const int64_t mean = M / G;
+    return mean > 160 ? 0 : mean > 64 ? 1 : mean > 16 || !rkc ? 2 : 3;
+}
+
+// Workgroups of a product over the slots: rows of R in tiles of br, slots in units (a group adds at
+// most one that is not full)
+static int64_t group_grid(int64_t M, int G, int64_t rows, int64_t br, int64_t unit)
+{
+    const int64_t units = M / unit + G < M ? M / unit + G : M;
+    return (units * ((rows + br - 1) / br) + 7) / 8 * 8;
+}
+
+static int64_t wgrad_grid(int G, int64_t N, int64_t K, int64_t b)
+{
+    return (((N + b - 1) / b) * ((K + b - 1) / b) + 7) / 8 * 8 * G;
+}
+
+// A launch has fewer than 2^32 threads. fwd: the products with k-contiguous weights.
+bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd)
+{
+    const int64_t most = ((int64_t)1 << 32) - 1;
+    const int plan = group_plan(M, G, fwd);
+    const int64_t rows = fwd ? N : K;
+    const int64_t br[4] = {256, 128, 128, 16}, unit[4] = {256, 128, 64, 16};
+    // (SwiGLU's F features in tiles of half as many are at most one tile of R more)
+    if ((group_grid(M, G, rows, br[plan], unit[plan]) + (M / unit[plan] + G)) > most / (plan == 3 ? 512 : 256)) return false;
+    return fwd || wgrad_grid(G, N, K, plan == 0 ? 256 : 128) <= most / 256;
+}
+
+template <typename T, bool RKC, int EPI, bool GATHER>
+static void group_launch(GroupArgs a, int64_t M, hipStream_t stream)
+{
+    const int64_t nr = EPI == FFN_SWIGLU ? a.p.F : a.p.Nr, br = EPI == FFN_SWIGLU ? T::BR / 2 : T::BR;
+    a.p.rtiles = (nr + br - 1) / br;
+    hipLaunchKernelGGL((k_group_gemm<T, RKC, EPI, GATHER>), dim3((unsigned)group_grid(M, a.G, nr, br, T::BC)), dim3(T::THREADS), 0,
+                       stream, a);
+}
+
+template <bool RKC, int EPI, bool GATHER>
+static void group_gemm(const GroupArgs& a, int64_t M, hipStream_t stream)
+{
+    const int plan = group_plan(M, a.G, RKC);
+    if constexpr (RKC) {
+        if (plan == 3) {
+            GroupArgs b = a;
+            const int64_t nr = EPI == FFN_SWIGLU ? a.p.F : a.p.Nr, br = EPI == FFN_SWIGLU ? 8 : 16;
+            b.p.rtiles = (nr + br - 1) / br;
+            hipLaunchKernelGGL((k_group_few<EPI, GATHER>), dim3((unsigned)group_grid(M, a.G, nr, br, 16)), dim3(512), 0, stream, b);
+            return;
+        }
+    }
+    if (plan == 0) group_launch<GroupLarge, RKC, EPI, GATHER>(a, M, stream);
+    else if (plan == 1) group_launch<GroupMid, RKC, EPI, GATHER>(a, M, stream);
+    else group_launch<GroupSlim, RKC, EPI, GATHER>(a, M, stream);
+}
+
+hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const uint16_t* w, const int64_t* offsets,
+                                 int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out, uint16_t* h13,
+                                 hipStream_t stream)
+{
+    const bool swi = epilogue == PMN_EPI_SWIGLU, f32 = epilogue == PMN_EPI_F32;
+    const int64_t F = N / 2;
+    GroupArgs a{FfnArgs{w, x, K, K, N, 0, K, out, nullptr, swi ? h13 : nullptr, F}, offsets, G, N * K, swi ? F : N, f32 ? 4 : 2, N};
+    a.p.gather = gather;
+    if (gather) {
+        if (swi) group_gemm<true, FFN_SWIGLU, true>(a, M, stream);
+        else if (f32) group_gemm<true, FFN_F32, true>(a, M, stream);
+        else group_gemm<true, FFN_BF16, true>(a, M, stream);
+    } else {
+        if (swi) group_gemm<true, FFN_SWIGLU, false>(a, M, stream);
+        else if (f32) group_gemm<true, FFN_F32, false>(a, M, stream);
+        else group_gemm<true, FFN_BF16, false>(a, M, stream);
+    }
+    return hipGetLastError();
+}
+
+// xg[s] = x[gather[s]], rows of K8 16-byte words: the operand that wgrad contracts over
+__global__ __launch_bounds__(256) void k_gather_rows(const uint4* __restrict__ x, const int32_t* __restrict__ gather,
+                                                     int64_t M, int64_t K8, uint4* __restrict__ xg)
+{
+    for (int64_t s = blockIdx.x; s < M; s += gridDim.x) {
+        const uint4* const from = x + (int64_t)gather[s] * K8;
+        for (int64_t k = threadIdx.x; k < K8; k += 256) xg[s * K8 + k] = from[k];
+    }
+}
+
+// da (or with h13: dh13 [M x 2K], and a [M x K] where it is not null) and dw, each where not null; xg:
+// rows in slot order for wgrad where gather is given
+hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
+                                 const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
+                                 void* da, bool da_f32, uint16_t* act, uint16_t* xg, void* dw, bool dw_f32,
+                                 hipStream_t stream)
+{
+    if (da && M > 0) {
+        GroupArgs a{FfnArgs{w, dy, K, N, K, 0, N, da, h13, act, K}, offsets, G, N * K, h13 ? 2 * K : K, da_f32 ? 4 : 2, K};
+        if (h13) group_gemm<false, FFN_SWIGLU_BWD, false>(a, M, stream);
+        else if (da_f32) group_gemm<false, FFN_F32, false>(a, M, stream);
+        else group_gemm<false, FFN_BF16, false>(a, M, stream);
+    }
+    if (dw) {
+        if (gather && M > 0) {
+            const int64_t K8 = K / 8;
+            hipLaunchKernelGGL(k_gather_rows, dim3((unsigned)(M < 16384 ? M : 16384)), dim3(256), 0, stream,
+                               reinterpret_cast<const uint4*>(x), gather, M, K8, reinterpret_cast<uint4*>(xg));
+            x = xg;
+        }
+        GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, dw, nullptr, nullptr, 0}, offsets, G, 0, 0, dw_f32 ? 4 : 2, 0};
+        auto run = [&](auto tile, auto epi) {
+            typedef decltype(tile) T;
+            a.p.rtiles = (K + T::BR - 1) / T::BR;
+            a.p.ctiles = (N + T::BC - 1) / T::BC;
+            hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value>), dim3((unsigned)wgrad_grid(G, N, K, T::BR)), dim3(T::THREADS),
+                               0, stream, a);
+        };
+        typedef std::integral_constant<int, FFN_F32> F32;
+        typedef std::integral_constant<int, FFN_BF16> BF16;
+        if (group_plan(M, G, false) == 0) {
+            if (dw_f32) run(GroupLarge{}, F32{});
+            else run(GroupLarge{}, BF16{});
+        } else {
+            if (dw_f32) run(GroupMid{}, F32{});
+            else run(GroupMid{}, BF16{});
+        }
+    }
+    return hipGetLastError();
+}
+
+}  // namespace pmn

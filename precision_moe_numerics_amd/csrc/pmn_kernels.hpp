@@ -162,6 +162,41 @@ hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t*
                           const uint16_t* h13, int64_t M, int64_t H, int64_t F, uint16_t* dh13, uint16_t* a,
                           float* part, uint16_t* dx, void* dw13, void* dw2, bool dw_f32, hipStream_t stream);
 
+// ---- the expert layer on unquantized activations ----------------------------------------------
+
+// Whether the launches of these sizes are within what a launch holds (fwd: the forward's, else the backward's)
+bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd);
+hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const uint16_t* w, const int64_t* offsets,
+                                 int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out, uint16_t* h13,
+                                 hipStream_t stream);
+// da (with h13: dh13 [M x 2K], and a [M x K] into act where it is not null) and dw, each where not null; xg
+// [M x K]: where wgrad's rows go in slot order (gather given)
+hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
+                                 const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
+                                 void* da, bool da_f32, uint16_t* act, uint16_t* xg, void* dw, bool dw_f32,
+                                 hipStream_t stream);
+
+int gemv_most_pairs();
+bool gemv_sums_at_once(int T, int k);
+// NVFP4 weights [G*N x K] times the rows of every pair of a token and an expert (x [T x K], per_pair: [T*k x K]):
+// out [T*k x N], SWIGLU [T*k x N/2]. ids null: matrix 0 (k = 1).
+hipError_t launch_gemv_pairs(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
+                             const float* outer, int64_t rpo, const int32_t* ids, int T, int k, int G, int64_t N,
+                             int64_t K, int epilogue, void* out, hipStream_t stream);
+// The pairs' sum with the gates (+ add) in one launch, where gemv_sums_at_once
+hipError_t launch_gemv_sum(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
+                           const float* outer, int64_t rpo, const int32_t* ids, const float* gates,
+                           const uint16_t* add, int T, int k, int G, int64_t N, int64_t K, bool f32, void* out,
+                           hipStream_t stream);
+
+// slot_of null: pair q is slot q; gates null: ones
+hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, const int32_t* slot_of,
+                               const float* gates, const uint16_t* add, int64_t T, int k, void* out, bool out_f32,
+                               hipStream_t stream);
+hipError_t launch_combine_rows_bwd(const void* dout, bool d_f32, const void* y, bool y_f32, int64_t M, int64_t H,
+                                   const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy,
+                                   float* dgates, hipStream_t stream);
+
 // The AdamW table on the device: this header, `count` entries, `chunks` chunk records.
 constexpr uint32_t ADAMW_MAGIC = 0x57414450u;
 struct AdamwTable {
