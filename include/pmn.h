@@ -488,9 +488,9 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
  *   expert's row), of fp32 (PMN_EPI_F32) or bf16; a pair whose id is outside [0, G) adds nothing.
  * PMN_EINVAL: gates with SWIGLU, add without gates. N % 32 == 0 (SWIGLU: N % 64 == 0), K % 32 == 0, N and K <=
  * 2^20, w_rows_per_outer % 32 == 0 (SWIGLU: F % w_rows_per_outer == 0 keeps w1 and w3 apart), T * k <= 4096
- * (PMN_ESHAPE). x, w_codes, add and out 16-byte aligned, w_scales 4. Workspace (16-byte aligned, at least
- * moe_gemv_nvfp4_workspace_size(T, k, N, gates != NULL) bytes, 0 for up to 16 tokens and 16 experts each;
- * PMN_EWORKSPACE; no initialization) holds the pairs' rows in fp32.
+ * (PMN_ESHAPE). x, w_codes, w_scales, add and out 16-byte aligned. Workspace (with gates; 16-byte aligned, at
+ * least moe_gemv_nvfp4_workspace_size(T, k, N, gates != NULL) bytes, PMN_EWORKSPACE; no initialization) holds
+ * the pairs' rows in fp32.
  */
 size_t moe_gemv_nvfp4_workspace_size(int64_t T, int k, int64_t N, int summed);
 int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const uint8_t* w_scales,

@@ -643,7 +643,7 @@ static bool bad_gemv_shape(int64_t T, int k, int G, int64_t N, int64_t K)
 
 size_t moe_gemv_nvfp4_workspace_size(int64_t T, int k, int64_t N, int summed)
 {
-    if (!summed || T <= 0 || k < 1 || N <= 0 || T > pmn::gemv_most_pairs() || pmn::gemv_sums_at_once((int)T, k)) return 0;
+    if (!summed || T <= 0 || k < 1 || N <= 0 || T > pmn::gemv_most_pairs()) return 0;
     return round256((size_t)(T * k * N) * 4);
 }
 
@@ -664,7 +664,7 @@ int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const 
     if (!x || !w_codes || !w_scales || !w_outer || !out) return PMN_EINVAL;
     const size_t need = moe_gemv_nvfp4_workspace_size(T, k, N, gates != nullptr);
     if (need > 0 && (!workspace || workspace_bytes < need)) return PMN_EWORKSPACE;
-    if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(w_outer, 4) || !aligned(ids, 4) ||
+    if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(w_outer, 4) || !aligned(ids, 4) ||
         !aligned(gates, 4) || !aligned(add, 16) || !aligned(out, 16) || (need > 0 && !aligned(workspace, 16)))
         return PMN_EALIGN;
     const uint16_t* xs = static_cast<const uint16_t*>(x);
@@ -672,14 +672,11 @@ int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const 
     if (!gates)
         return status(pmn::launch_gemv_pairs(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids, (int)T,
                                              k, G, N, K, epilogue, out, hs(stream)));
-    const bool f32 = epilogue == PMN_EPI_F32;
-    if (need == 0)
-        return status(pmn::launch_gemv_sum(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids, gates,
-                                           as, (int)T, k, G, N, K, f32, out, hs(stream)));
     const hipError_t e = pmn::launch_gemv_pairs(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids,
                                                 (int)T, k, G, N, K, PMN_EPI_F32, workspace, hs(stream));
     if (e != hipSuccess) return PMN_ELAUNCH;
-    return status(pmn::launch_combine_rows(workspace, true, T * k, N, nullptr, gates, as, T, k, out, f32, hs(stream)));
+    return status(pmn::launch_combine_rows(workspace, true, T * k, N, nullptr, gates, as, T, k, out,
+                                           epilogue == PMN_EPI_F32, hs(stream)));
 }
 
 static bool bad_rows_shape(int64_t M, int64_t H, int64_t T, int k)

@@ -1,19 +1,24 @@
 // gemv.hip -- products of a few tokens' bf16 activations with NVFP4 weights, for decoding:
 //     y[t, j, n] = outer(r) sum_k x[t (, j), k] fp4(r, k) e4m3(r, k / 16),   r = ids[t, j] N + n
-// per pair (t, j) of a token and its j-th expert (k_gemv_pairs: fp32, bf16, or SwiGLU with N = 2F), or
-// summed over a token's experts with its gates (k_gemv_sum).
+// per pair (t, j) of a token and its j-th expert, in fp32, bf16, or through SwiGLU (N = 2F).
 //
-// Arithmetic. fp4 * e4m3 has at most 6 significant bits and is exact in bf16, so the weights go to
-// v_mfma_f32_16x16x32_bf16 as bf16 (one conversion to two fp32, two products by the block's scale, one
-// packed conversion for two weights) and every product is exact; sums are fp32, outer scales and gates
-// multiply the sums.
+// What bounds it: the weights' bytes from HBM, 9/16 of a byte each; next to them the vector instructions
+// that unpack the codes (a CU has about 126 of them for 1 KB of codes at 5 TB/s).
 //
-// What bounds it: the weights' bytes from HBM, 9/16 of a byte each. A workgroup holds 16 rows of a matrix
-// (SwiGLU: 8 features of w1 and the same of w3) and its 8 wavefronts share the contraction in units of
-// 128 k, 64 bytes of codes of each row: lane (g, i) loads 16 bytes of row i, the 32 values 32 g .. of the
-// unit, with their two scale bytes; its 8 values of MFMA step s are 32 g + 8 s .., for both operands, so
-// nothing is exchanged between lanes. Activations come from L2 straight to registers. The wavefronts' sums
-// are added in order through LDS: results do not depend on the launch, and a column's not on the others.
+// Split. A workgroup holds RT tiles of 16 rows of one expert's matrix (SwiGLU: 8 features of w1 and the same
+// of w3) and all pairs that name the expert; its wavefronts share the contraction in units of 128 k, 64 bytes
+// of codes of each row, dealt in turn: lane (g, i) loads the 16 bytes of row i that hold the unit's values
+// 32 g .. 32 g + 31, one unit ahead of its use. The tiles' scales go through LDS in 16-byte pieces (loaded from
+// memory per unit, 2 bytes a lane, they took a quarter of the time: one token through 8 experts of 4096 x 7168
+// 37 us, 27 without any scales). The wavefronts' sums are added in order through LDS, so results do not
+// depend on the launch.
+//
+// Up to two pairs (one decoded token): codes become bf16 exactly in one conversion for two, v_dot2_f32_bf16
+// multiplies them with x from LDS, and a block's sum of 16 is multiplied by its scale once: 36 vector
+// instructions for 32 weights and one pair. More pairs: fp4 * e4m3 has at most 6 significant bits and is exact
+// in bf16 (two conversions and two products for two weights), for v_mfma_f32_16x16x32_bf16 with up to 16
+// pairs as columns; more than 16 take the weights again, from the caches. Products are exact and sums fp32
+// either way; the outer scales multiply the sums.
 #include <type_traits>
 
 #include "pmn_dev.hpp"
@@ -32,49 +37,37 @@ struct GemvArgs {
     const float* outer;
     int64_t rpo;
     const int32_t* ids;       // [T*k], or null: matrix 0
-    const float* gates;       // k_gemv_sum
-    const uint16_t* add;      // k_gemv_sum: bf16 [T x N] or null
-    int T, k, G, pairs;       // pairs = T * k
+    int k, G, pairs;
     int by_pair;              // workgroups go by pairs (the first of each expert works) or by experts
     int64_t N, K, F;
-    int rblocks;
-    void* out;
+    int rblocks;              // workgroups a matrix
+    void* out;                // [pairs x N], SwiGLU [pairs x F]
 };
 
-constexpr int GEMV_PAIRS = 4096;   // most pairs of a call
-constexpr int GEMV_W = 8;          // wavefronts of a workgroup
+constexpr int GEMV_PAIRS = 4096;    // most pairs of a call
+constexpr int GEMV_CHUNK = 8192;    // k whose scales (and x of two pairs) stand in LDS at a time
+constexpr int GEMV_FEW = 2;         // pairs that go through dot2: a third and fourth in LDS would leave one workgroup a CU
 
-// One unit of a lane: its codes and scales
-struct GemvWeights {
-    u32x4 c;
-    uint32_t s;
-};
-PMN_DEV GemvWeights gemv_load(const uint8_t* codes, const uint8_t* scales, int64_t k, int64_t K)
+static __device__ const uint4 gemv_zeros[4] = {};   // x past K: 32 values
+
+PMN_DEV float dot2(uint32_t a, uint32_t b, float c)
 {
-    GemvWeights w{};
-    if (k < K) {   // K % 32 == 0: a lane's 32 values are all inside or all outside
-        w.c = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + (k >> 1)));
-        w.s = *reinterpret_cast<const uint16_t*>(scales + (k >> 4));
-    }
-    return w;
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
 }
 
-// The 8 weights of step s as bf16
-PMN_DEV bf16x8 gemv_values(const GemvWeights& w, int s)
+// Byte `sel` of a code word as two bf16
+#define PMN_FP4_TO_BF16(w, sel) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((w), 1.0f, (sel)))
+
+// 8 codes times their scale d as bf16
+PMN_DEV bf16x8 gemv_values(uint32_t codes, float d)
 {
-    const float d = e4m3_value((w.s >> (8 * (s >> 1))) & 0xFFu);
     float v[8];
-    deq8(w.c[s], d, v);
+    deq8(codes, d, v);
     const u32x4 b = {bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])};
     return __builtin_bit_cast(bf16x8, b);
 }
 
-PMN_DEV bf16x8 gemv_x(const uint16_t* x, int64_t k, int64_t K)
-{
-    return k < K ? *reinterpret_cast<const bf16x8*>(x + k) : bf16x8{};
-}
-
-// Rows of a pair's outputs that nothing computes (an id outside [0, G)): zeros.
+// Outputs r0 .. of a pair that no expert computes (an id outside [0, G)): zeros.
 PMN_DEV void gemv_zero(const GemvArgs& p, int pair, int64_t r0, int width, int64_t rows, int bytes)
 {
     for (int i = threadIdx.x; i < width; i += blockDim.x)
@@ -84,297 +77,321 @@ PMN_DEV void gemv_zero(const GemvArgs& p, int pair, int64_t r0, int width, int64
         }
 }
 
-// A workgroup: 16 rows of one expert's matrix times the rows of all pairs that name it, in passes of
-// 16 CT columns.
-template <int EPI, int CT>
-__global__ __launch_bounds__(GEMV_W * 64, 2) void k_gemv_pairs(GemvArgs p)
+template <int EPI, int RT, int W>
+__global__ __launch_bounds__(W * 64, 4) void k_gemv(GemvArgs p, int pitch, int list0)
 {
     constexpr bool SWI = EPI == PMN_EPI_SWIGLU;
-    constexpr int W = GEMV_W, U = CT == 1 ? 4 : 2;
-    __shared__ float4 red[W][CT][64];
-    __shared__ uint16_t list[GEMV_PAIRS];
+    constexpr int RS = SWI ? 8 : 16, OB = EPI == PMN_EPI_F32 ? 4 : 2, THREADS = W * 64;
+    // scales [RT * 16][pitch], then x of up to GEMV_FEW pairs in whole units; in their place at the end, the
+    // wavefronts' sums red[W][RT][column][row]. From list0 the pairs of the expert.
+    extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
     __shared__ int found[W];
+    float (*red)[RT][16][16] = reinterpret_cast<float (*)[RT][16][16]>(dyn);
+    uint16_t* const list = reinterpret_cast<uint16_t*>(dyn + list0);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     const int d = blockIdx.x / p.rblocks;
-    const int64_t r0 = (int64_t)(blockIdx.x - d * p.rblocks) * (SWI ? 8 : 16);
+    const int64_t r0 = (int64_t)(blockIdx.x - d * p.rblocks) * (RT * RS);
     const int64_t rows = SWI ? p.F : p.N;
-    constexpr int OB = EPI == PMN_EPI_F32 ? 4 : 2;
-    const int e = !p.ids ? 0 : p.by_pair ? __builtin_amdgcn_readfirstlane(p.ids[d]) : d;
-    if (e < 0 || e >= p.G) {   // by pairs only
-        gemv_zero(p, d, r0, SWI ? 8 : 16, rows, OB);
-        return;
-    }
-    int64_t row = SWI ? r0 + (l16 & 7) : r0 + l16;
-    if (SWI && l16 >= 8) row += p.F;
-    const int64_t at = (int64_t)e * p.N + row;
-    const uint8_t* const codes = p.codes + at * (p.K >> 1);
-    const uint8_t* const scales = p.scales + at * (p.K >> 4);
-    const int64_t units = (p.K + 127) >> 7;
+    const int K = (int)p.K;
 
-    // the pairs of this expert are listed in their order; a dense product's first weights are on their way
-    // by then (an expert that no pair names reads nothing)
-    GemvWeights w[U];
-    auto load_weights = [&](int64_t u) {
+    // this workgroup's expert, and the pairs that name it in their order
+    int e = 0, n = p.pairs;
+    if (p.ids && p.pairs <= 64) {
+        const int id = lane < p.pairs ? p.ids[lane] : -1;
+        e = p.by_pair ? __builtin_amdgcn_readlane(id, d) : d;
+        if (e < 0 || e >= p.G) {   // by pairs only
+            gemv_zero(p, d, r0, RT * RS, rows, OB);
+            return;
+        }
+        if (!p.by_pair && d == 0) {
+            uint64_t none = __ballot(lane < p.pairs && (id < 0 || id >= p.G));
+            for (; none; none &= none - 1) gemv_zero(p, __builtin_ctzll(none), r0, RT * RS, rows, OB);
+        }
+        const uint64_t all = __ballot(id == e);
+        if (all == 0 || (p.by_pair && __builtin_ctzll(all) != d)) return;   // an expert's first pair works for all
+        n = __popcll(all);
+        if (wave == 0 && id == e) list[__popcll(all & ((1ull << lane) - 1ull))] = (uint16_t)lane;
+    } else if (p.ids) {
+        e = p.by_pair ? __builtin_amdgcn_readfirstlane(p.ids[d]) : d;
+        if (e < 0 || e >= p.G) {
+            gemv_zero(p, d, r0, RT * RS, rows, OB);
+            return;
+        }
+        n = 0;
+        for (int base = 0; base < p.pairs; base += THREADS) {
+            const int q = base + tid;
+            const int id = q < p.pairs ? p.ids[q] : 0;
+            const bool hit = q < p.pairs && id == e;
+            const uint64_t all = __ballot(hit);
+            if (lane == 0) found[wave] = __popcll(all);
+            __syncthreads();
+            int before = n;
 #pragma unroll
-        for (int i = 0; i < U; i++) w[i] = gemv_load(codes, scales, (u + W * i) * 128 + 32 * g, p.K);
+            for (int v = 0; v < W; v++) {
+                if (v < wave) before += found[v];
+                n += found[v];
+            }
+            if (hit) list[before + __popcll(all & ((1ull << lane) - 1ull))] = (uint16_t)q;
+            __syncthreads();
+            if (!p.by_pair && d == 0 && __syncthreads_or(q < p.pairs && (id < 0 || id >= p.G))) {
+                for (int b = base; b < base + THREADS && b < p.pairs; b++)
+                    if (p.ids[b] < 0 || p.ids[b] >= p.G) gemv_zero(p, b, r0, RT * RS, rows, OB);
+            }
+        }
+        if (n == 0 || (p.by_pair && list[0] != d)) return;
+        n = __builtin_amdgcn_readfirstlane(n);
+    }
+
+    // rows of tile t, from the matrix' first (tiles past it repeat its first rows and are not stored)
+    const uint8_t* base[RT];
+#pragma unroll
+    for (int t = 0; t < RT; t++)
+        base[t] = p.codes + ((int64_t)e * p.N + (r0 + t * RS < rows ? r0 + t * RS : 0)) * (p.K >> 1);
+    const uint32_t roff = (uint32_t)((SWI ? (l16 & 7) + (l16 >> 3) * p.F : l16) * (p.K >> 1));
+    struct Batch {
+        u32x4 c[RT];
     };
-    if (!p.ids) load_weights(wave);
-    int n = 0;
-    for (int base = 0; base < p.pairs; base += W * 64) {
-        const int q = base + tid;
-        const int id = q < p.pairs ? (p.ids ? p.ids[q] : 0) : -1;
-        const bool hit = q < p.pairs && id == e;
-        const uint64_t all = __ballot(hit);
-        if (lane == 0) found[wave] = __popcll(all);
-        __syncthreads();
-        int before = n;
+    auto load = [&](int u, Batch& b) {   // unit u; lanes past K read the row's last 32 again, times zeros
+        int k = u * 128 + 32 * g;
+        k = k < K ? k : K - 32;
 #pragma unroll
-        for (int v = 0; v < W; v++) {
-            if (v < wave) before += found[v];
-            n += found[v];
-        }
-        if (hit) list[before + __popcll(all & ((1ull << lane) - 1ull))] = (uint16_t)q;
-        __syncthreads();
-        if (!p.by_pair && d == 0 && __syncthreads_or(q < p.pairs && (id < 0 || id >= p.G))) {
-            for (int b = base; b < base + W * 64 && b < p.pairs; b++)
-                if (p.ids[b] < 0 || p.ids[b] >= p.G) gemv_zero(p, b, r0, SWI ? 8 : 16, rows, OB);
-        }
-    }
-    if (n == 0 || (p.by_pair && list[0] != d)) return;   // an expert's first pair works for all
-    if (p.ids) load_weights(wave);
+        for (int t = 0; t < RT; t++) b.c[t] = *reinterpret_cast<const u32x4*>(base[t] + (roff + (uint32_t)(k >> 1)));
+    };
+    // the scales of k0 .. k0 + kn of all tiles' rows; rows begin at multiples of K / 16 bytes
+    auto stage_scales = [&](int k0, int kn) {
+        auto copy = [&](auto unit) {
+            typedef decltype(unit) U;
+            const int per = (kn >> 4) / (int)sizeof(U);
+            for (int i = tid; i < RT * 16 * per; i += THREADS) {
+                const int r = i / per, c = i - r * per, t = r >> 4;
+                const int64_t first = r0 + t * RS < rows ? r0 + t * RS : 0;
+                const int64_t row = (int64_t)e * p.N + first + (SWI ? (r & 7) + ((r >> 3) & 1) * p.F : r & 15);
+                reinterpret_cast<U*>(dyn + r * pitch)[c] = reinterpret_cast<const U*>(p.scales + row * (p.K >> 4) + (k0 >> 4))[c];
+            }
+        };
+        if (K % 256 == 0) copy(uint4{});
+        else if (K % 64 == 0) copy(uint32_t{});
+        else copy(uint16_t{});
+    };
+    // the two scales of this lane's 32 values of unit u (of its chunk) in tile t; not staged past K
+    const uint8_t* const srow = dyn + l16 * pitch + 2 * g;
+    auto scale_of = [&](int u, int t) -> uint32_t { return *reinterpret_cast<const uint16_t*>(srow + t * 16 * pitch + u * 8); };
 
-    for (int c0 = 0; c0 < n; c0 += 16 * CT) {
-        const uint16_t* xp[CT];
-        bool in[CT];
+    // sums of columns c0 .. c0 + nc - 1 from red
+    auto finish = [&](int c0, int nc) {
+        __syncthreads();
+        for (int z = tid; z < RT * nc * (RS / 4); z += THREADS) {
+            const int q = z % (RS / 4), c = z / (RS / 4) % nc, t = z / (RS / 4) / nc;
+            const int64_t r = r0 + t * RS + 4 * q;
+            if (r >= rows) continue;
+            const int64_t pair = p.ids ? list[c0 + c] : c0 + c;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v3[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int t = 0; t < CT; t++) {
-            in[t] = c0 + 16 * t < n;   // uniform
-            const int c = c0 + 16 * t + l16 < n ? c0 + 16 * t + l16 : n - 1;   // columns past the last repeat it
-            const int pair = list[c];
-            xp[t] = p.x + (int64_t)(p.per_pair ? pair : pair / p.k) * p.K;
-        }
-        f32x4 acc[CT];
-#pragma unroll
-        for (int t = 0; t < CT; t++) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (c0 > 0) load_weights(wave);
-        for (int64_t u = wave; u < units; u += W * U) {
-            GemvWeights cur[U];
-#pragma unroll
-            for (int i = 0; i < U; i++) cur[i] = w[i];
-            load_weights(u + W * U);
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                const int64_t k = (u + W * i) * 128 + 32 * g;
-                if ((u + W * i) >= units) break;
-                bf16x8 x[CT][4];
-#pragma unroll
-                for (int t = 0; t < CT; t++)
-                    if (in[t])
-#pragma unroll
-                        for (int s = 0; s < 4; s++) x[t][s] = gemv_x(xp[t], k < p.K ? k + 8 * s : p.K, p.K);
-#pragma unroll
-                for (int s = 0; s < 4; s++) {
-                    const bf16x8 v = gemv_values(cur[i], s);
-#pragma unroll
-                    for (int t = 0; t < CT; t++)
-                        if (in[t]) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, x[t][s], acc[t], 0, 0, 0);
+            for (int w = 0; w < W; w++) {
+                const float4 s = *reinterpret_cast<const float4*>(&red[w][t][c][4 * q]);
+                v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
+                if (SWI) {
+                    const float4 s3 = *reinterpret_cast<const float4*>(&red[w][t][c][8 + 4 * q]);
+                    v3[0] += s3.x; v3[1] += s3.y; v3[2] += s3.z; v3[3] += s3.w;
                 }
             }
-        }
-        if (c0 > 0) __syncthreads();
-#pragma unroll
-        for (int t = 0; t < CT; t++)
-            if (in[t]) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-        __syncthreads();
-        // wavefront t finishes column tile t: lane l rows 4 (l / 16) .. +3 of column l % 16
-        if (wave < CT && c0 + 16 * wave < n) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int q = 0; q < W; q++) {
-                const float4 s = red[q][wave][lane];
-                v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
-            }
-            const int c = c0 + 16 * wave + l16;
-            // rows_per_outer is a multiple of 32: one scale for the rows of a workgroup's matrix
-            const int64_t first = (int64_t)e * p.N + r0 + (SWI && g >= 2 ? p.F : 0);
-            const float o = p.outer[first / p.rpo];
+            const float o = p.outer[((int64_t)e * p.N + r) / p.rpo];
 #pragma unroll
             for (int i = 0; i < 4; i++) v[i] *= o;
             if (SWI) {
-                // lanes 0 .. 31 hold h1 of 8 features, lanes 32 .. 63 their h3
-                float a[4];
+                const float o3 = p.outer[((int64_t)e * p.N + p.F + r) / p.rpo];
 #pragma unroll
-                for (int i = 0; i < 4; i++) a[i] = silu(v[i]) * __shfl_xor(v[i], 32, 64);
-                if (g < 2 && c < n)
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)list[c] * p.F + r0 + 4 * g) =
-                        make_uint2(bf16x2_bits(a[0], a[1]), bf16x2_bits(a[2], a[3]));
-            } else if (c < n) {
-                const int64_t o4 = (int64_t)list[c] * p.N + r0 + 4 * g;
-                if (EPI == PMN_EPI_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o4) = make_float4(v[0], v[1], v[2], v[3]);
-                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o4) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+                for (int i = 0; i < 4; i++) v[i] = silu(v[i]) * (v3[i] * o3);
+            }
+            if (EPI == PMN_EPI_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + pair * rows + r) = make_float4(v[0], v[1], v[2], v[3]);
+            else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + pair * rows + r) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+        }
+    };
+
+    // Chunks of the contraction with their scales in LDS (one for K up to GEMV_CHUNK), then this wavefront's
+    // units of it with the next one's codes on their way. before(k0, kn) stages what else the chunk needs.
+    auto contract = [&](auto before, auto compute) {
+        for (int k0 = 0; k0 < K; k0 += GEMV_CHUNK) {
+            const int kn = K - k0 < GEMV_CHUNK ? K - k0 : GEMV_CHUNK, u0 = k0 >> 7, un = (kn + 127) >> 7;
+            Batch a, b;
+            if (wave < un) load(u0 + wave, a);
+            if (k0 > 0) __syncthreads();
+            stage_scales(k0, kn);
+            before(k0, kn);
+            __syncthreads();
+            for (int u = wave; u < un;) {
+                if (u + W < un) load(u0 + u + W, b);
+                compute(u0 + u, u, a);
+                u += W;
+                if (u >= un) break;
+                if (u + W < un) load(u0 + u + W, a);
+                compute(u0 + u, u, b);
+                u += W;
             }
         }
-    }
-}
+    };
 
-// out[t, n] = sum_j gates[t, j] y[t, j, n] (+ add[t, n]) for up to 16 tokens: a workgroup holds 16 rows n of
-// every expert that is named and adds its experts' sums, each with its tokens' gates, before the
-// wavefronts' are joined. The work is a list of (expert, occurrence in its token): a token that names an
-// expert twice has it in two entries. Its units go round the wavefronts, so one token's 8 experts of 2048
-// k keep all of them at work.
-template <bool F32OUT>
-__global__ __launch_bounds__(GEMV_W * 64, 2) void k_gemv_sum(GemvArgs p)
-{
-    constexpr int W = GEMV_W, U = 4, MOST = 256;
-    __shared__ float4 red[W][64];
-    __shared__ int32_t id[MOST], key[MOST];
-    __shared__ int16_t map[MOST][16];   // entry, token -> pair or -1
-    __shared__ int32_t expert[MOST];
-    __shared__ int found[W];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
-    const int64_t r0 = (int64_t)blockIdx.x * 16;
-    // pair q: its expert and which of its token's pairs with that expert it is
-    int mine = -1;
-    if (tid < p.pairs) {
-        mine = p.ids ? p.ids[tid] : 0;
-        if (mine < 0 || mine >= p.G) mine = -1;
-        id[tid] = mine;
-    }
-    for (int i = tid; i < MOST * 16 / 2; i += W * 64) reinterpret_cast<uint32_t*>(map)[i] = 0xFFFFFFFFu;
-    __syncthreads();
-    int k = -1;
-    if (mine >= 0) {
-        int rank = 0;
-        for (int q = tid / p.k * p.k; q < tid; q++) rank += id[q] == mine;
-        k = mine * 16 + rank;   // at most 16 pairs a token
-    }
-    if (tid < p.pairs) key[tid] = k;
-    __syncthreads();
-    int first = tid;
-    if (k >= 0)
-        for (int q = 0; q < tid; q++)
-            if (key[q] == k) {
-                first = q;
-                break;
-            }
-    const bool leads = k >= 0 && first == tid;
-    const uint64_t all = __ballot(leads);
-    if (lane == 0) found[wave] = __popcll(all);
-    __syncthreads();
-    int before = 0, entries = 0;
+    if (n <= GEMV_FEW) {
+        uint8_t* const xs = dyn + RT * 16 * pitch;
+        constexpr int XROW = GEMV_CHUNK * 2;
+        const int xrow = K < GEMV_CHUNK ? ((K + 127) >> 7) * 256 : XROW;
+        auto run = [&](auto cols) {
+            constexpr int C = decltype(cols)::value;
+            float acc[C][RT];
 #pragma unroll
-    for (int v = 0; v < W; v++) {
-        if (v < wave) before += found[v];
-        entries += found[v];
-    }
-    before += __popcll(all & ((1ull << lane) - 1ull));
-    if (leads) {
-        expert[before] = mine;
-        id[tid] = before;   // the entry of the pairs that tid leads
-    }
-    __syncthreads();
-    if (k >= 0) map[id[first]][tid / p.k] = (int16_t)tid;
-    __syncthreads();
-
-    const int units = (int)((p.K + 127) >> 7);
-    const int items = entries * units;
-    f32x4 total = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int it = wave; it < items; it += W * U) {
-        GemvWeights w[U];
-        bf16x8 x[U][4];
-        float scale[U];
-        bool on[U];   // the lane's token names the entry's expert: nothing is added otherwise, NaN scales neither
+            for (int c = 0; c < C; c++)
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int item = it + W * i;
-            w[i] = GemvWeights{};
-            scale[i] = 0.0f;
-            on[i] = false;
+                for (int t = 0; t < RT; t++) acc[c][t] = 0.0f;
+            contract(
+                [&](int k0, int kn) {
+                    if (k0 == 0 && p.ids && p.pairs <= 64) __syncthreads();   // list
 #pragma unroll
-            for (int s = 0; s < 4; s++) x[i][s] = bf16x8{};
-            if (item < items) {
-                const int d = item / units;
-                const int64_t kk = (int64_t)(item - d * units) * 128 + 32 * g;
-                const int64_t at = (int64_t)__builtin_amdgcn_readfirstlane(expert[d]) * p.N + r0;
-                w[i] = gemv_load(p.codes + (at + l16) * (p.K >> 1), p.scales + (at + l16) * (p.K >> 4), kk, p.K);
-                const int pair = map[d][l16];
-                if (pair >= 0) {
-                    on[i] = true;
-                    scale[i] = p.gates[pair] * p.outer[at / p.rpo];
-                    const uint16_t* const xp = p.x + (int64_t)(p.per_pair ? pair : pair / p.k) * p.K;
+                    for (int c = 0; c < C; c++) {
+                        const int pair = p.ids ? list[c] : c;
+                        const uint16_t* const x = p.x + (int64_t)(p.per_pair ? pair : pair / p.k) * p.K + k0;
+                        for (int i = tid; i < ((kn + 127) >> 7) * 16; i += THREADS)
+                            *reinterpret_cast<uint4*>(xs + c * xrow + i * 16) =
+                                i * 8 < kn ? *reinterpret_cast<const uint4*>(x + i * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                },
+                [&](int uk, int u, const Batch& b) {
+                    const bool in = uk * 128 + 32 * g < K;
+                    uint32_t s[RT];
 #pragma unroll
-                    for (int s = 0; s < 4; s++) x[i][s] = gemv_x(xp, kk < p.K ? kk + 8 * s : p.K, p.K);
+                    for (int t = 0; t < RT; t++) s[t] = in ? scale_of(u, t) : 0u;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {   // the lane's two blocks of 16
+                        uint4 x[C][2];
+#pragma unroll
+                        for (int c = 0; c < C; c++)
+#pragma unroll
+                            for (int q = 0; q < 2; q++)
+                                x[c][q] = *reinterpret_cast<const uint4*>(xs + c * xrow + u * 256 + g * 64 + h * 32 + q * 16);
+#pragma unroll
+                        for (int t = 0; t < RT; t++) {
+                            const float d16 = e4m3_value((s[t] >> (8 * h)) & 0xFFu);
+                            uint32_t v[8];
+#pragma unroll
+                            for (int q = 0; q < 2; q++) {
+                                const uint32_t w = b.c[t][2 * h + q];
+                                v[4 * q] = PMN_FP4_TO_BF16(w, 0);
+                                v[4 * q + 1] = PMN_FP4_TO_BF16(w, 1);
+                                v[4 * q + 2] = PMN_FP4_TO_BF16(w, 2);
+                                v[4 * q + 3] = PMN_FP4_TO_BF16(w, 3);
+                            }
+#pragma unroll
+                            for (int c = 0; c < C; c++) {
+                                float sum = 0.0f;
+#pragma unroll
+                                for (int q = 0; q < 2; q++) {
+                                    sum = dot2(v[4 * q], x[c][q].x, sum);
+                                    sum = dot2(v[4 * q + 1], x[c][q].y, sum);
+                                    sum = dot2(v[4 * q + 2], x[c][q].z, sum);
+                                    sum = dot2(v[4 * q + 3], x[c][q].w, sum);
+                                }
+                                acc[c][t] = __builtin_fmaf(sum, d16, acc[c][t]);
+                            }
+                        }
+                    }
+                });
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int t = 0; t < RT; t++) {
+                    float v = acc[c][t];
+                    v += __shfl_xor(v, 16, 64);
+                    v += __shfl_xor(v, 32, 64);
+                    acc[c][t] = v;
                 }
-            }
-        }
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            if (it + W * i >= items) break;
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int s = 0; s < 4; s++) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gemv_values(w[i], s), x[i][s], acc, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < 4; q++) total[q] = on[i] ? __builtin_fmaf(acc[q], scale[i], total[q]) : total[q];
-        }
+                for (int t = 0; t < RT; t++)
+                    if (g == 0) red[wave][t][c][l16] = acc[c][t];
+        };
+        if (n == 1) run(std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, 2>{});
+        finish(0, n);
+        return;
     }
-    red[wave][lane] = make_float4(total[0], total[1], total[2], total[3]);
-    __syncthreads();
-    if (wave > 0 || l16 >= p.T) return;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (p.ids && p.pairs <= 64) __syncthreads();   // list
+    for (int c0 = 0; c0 < n; c0 += 16) {
+        const int c = c0 + l16 < n ? c0 + l16 : n - 1;   // columns past the last repeat it
+        const int pair = p.ids ? list[c] : c;
+        const uint16_t* const xp = p.x + (int64_t)(p.per_pair ? pair : pair / p.k) * p.K;
+        f32x4 acc[RT];
 #pragma unroll
-    for (int q = 0; q < W; q++) {
-        const float4 s = red[q][lane];
-        v[0] += s.x; v[1] += s.y; v[2] += s.z; v[3] += s.w;
+        for (int t = 0; t < RT; t++) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (c0 > 0) __syncthreads();
+        contract([](int, int) {},
+                 [&](int uk, int u, const Batch& b) {
+                     const int k = uk * 128 + 32 * g;
+                     const bool in = k < K;
+                     const uint16_t* const x = in ? xp + k : reinterpret_cast<const uint16_t*>(gemv_zeros);
+                     bf16x8 f[4];
+#pragma unroll
+                     for (int s = 0; s < 4; s++) f[s] = *reinterpret_cast<const bf16x8*>(x + 8 * s);
+#pragma unroll
+                     for (int t = 0; t < RT; t++) {
+                         const uint32_t sc = in ? scale_of(u, t) : 0u;
+#pragma unroll
+                         for (int s = 0; s < 4; s++)
+                             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                 gemv_values(b.c[t][s], e4m3_value((sc >> (8 * (s >> 1))) & 0xFFu)), f[s], acc[t], 0, 0, 0);
+                     }
+                 });
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < RT; t++)
+            *reinterpret_cast<float4*>(&red[wave][t][l16][4 * g]) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        finish(c0, n - c0 < 16 ? n - c0 : 16);
     }
-    const int64_t o = l16 * p.N + r0 + 4 * g;
-    if (p.add) {
-        const uint2 a = *reinterpret_cast<const uint2*>(p.add + o);
-        v[0] += bf16_lo(a.x); v[1] += bf16_hi(a.x); v[2] += bf16_lo(a.y); v[3] += bf16_hi(a.y);
-    }
-    if (F32OUT) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
-    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
 }
 
 int gemv_most_pairs() { return GEMV_PAIRS; }
-bool gemv_sums_at_once(int T, int k) { return T <= 16 && k <= 16; }
 
 // y of every pair: [T*k x N], SwiGLU [T*k x N/2]
 hipError_t launch_gemv_pairs(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
                              const float* outer, int64_t rpo, const int32_t* ids, int T, int k, int G, int64_t N,
                              int64_t K, int epilogue, void* out, hipStream_t stream)
 {
-    GemvArgs p{x, per_pair, codes, scales, outer, rpo, ids, nullptr, nullptr, T, k, G, T * k, 0, N, K, N / 2, 0, out};
+    GemvArgs p{x, per_pair, codes, scales, outer, rpo, ids, k, G, T * k, 0, N, K, N / 2, 0, out};
     p.by_pair = ids && p.pairs < G;
-    p.rblocks = (int)(epilogue == PMN_EPI_SWIGLU ? p.F / 8 : N / 16);
     const int experts = !ids ? 1 : p.by_pair ? p.pairs : G;
-    const dim3 grid((unsigned)(experts * p.rblocks)), block(GEMV_W * 64);
-    // columns of an expert: one tile of 16 where no more tokens are there
-    if (T <= 16) {
-        if (epilogue == PMN_EPI_SWIGLU) hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_SWIGLU, 1>), grid, block, 0, stream, p);
-        else if (epilogue == PMN_EPI_F32) hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_F32, 1>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_BF16, 1>), grid, block, 0, stream, p);
-    } else {
-        if (epilogue == PMN_EPI_SWIGLU) hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_SWIGLU, 4>), grid, block, 0, stream, p);
-        else if (epilogue == PMN_EPI_F32) hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_F32, 4>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((k_gemv_pairs<PMN_EPI_BF16, 4>), grid, block, 0, stream, p);
-    }
-    return hipGetLastError();
-}
-
-// The gates' sum over up to 16 tokens and 16 experts each (gemv_sums_at_once)
-hipError_t launch_gemv_sum(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
-                           const float* outer, int64_t rpo, const int32_t* ids, const float* gates,
-                           const uint16_t* add, int T, int k, int G, int64_t N, int64_t K, bool f32, void* out,
-                           hipStream_t stream)
-{
-    GemvArgs p{x, per_pair, codes, scales, outer, rpo, ids, gates, add, T, k, G, T * k, 0, N, K, 0, (int)(N / 16), out};
-    const dim3 grid((unsigned)(N / 16)), block(GEMV_W * 64);
-    if (f32) hipLaunchKernelGGL((k_gemv_sum<true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((k_gemv_sum<false>), grid, block, 0, stream, p);
+    const int64_t tiles = epilogue == PMN_EPI_SWIGLU ? p.F / 8 : N / 16;
+    // Wavefronts: a contraction of up to 4096 leaves 8 of them too few units each (5 tokens through 8 experts
+    // of 7168 x 2048: 74 us with 8, 52 with 4; one of 4096 x 7168: 27 us with 8, 32 with 4). Tiles: three
+    // where four rounds of workgroups are there (61 tokens, 4096 x 7168: 233 us with two, 212 with three: x is
+    // read from L2 less often), two else (one token: 28 us with two, 30 with three), one where two would leave
+    // CUs without a workgroup.
+    const int w = K <= 4096 ? 4 : 8;
+    auto groups = [&](int r) { return experts * ((tiles + r - 1) / r); };
+    const int rt = groups(3) >= 4 * 256 * 16 / w ? 3 : groups(2) >= 512 ? 2 : 1;
+    p.rblocks = (int)((tiles + rt - 1) / rt);
+    const int chunk = K < GEMV_CHUNK ? (int)((K + 127) / 128 * 128) : GEMV_CHUNK;
+    const int pitch = chunk / 16 + 16;   // 16 rows a dword apart hit different banks
+    const int sums = w * rt * 1024, staged = rt * 16 * pitch + GEMV_FEW * chunk * 2, list0 = staged > sums ? staged : sums;
+    const size_t lds = list0 + (p.pairs * 2 + 15) / 16 * 16;
+    const dim3 grid((unsigned)(experts * p.rblocks)), block(w * 64);
+    auto go = [&](auto epi, auto r, auto waves) {
+        hipLaunchKernelGGL((k_gemv<decltype(epi)::value, decltype(r)::value, decltype(waves)::value>), grid, block, lds, stream, p, pitch, list0);
+    };
+    auto by_shape = [&](auto epi) {
+        const std::integral_constant<int, 1> one;
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 3> three;
+        const std::integral_constant<int, 4> four;
+        const std::integral_constant<int, 8> eight;
+        if (w == 4) rt == 3 ? go(epi, three, four) : rt == 2 ? go(epi, two, four) : go(epi, one, four);
+        else rt == 3 ? go(epi, three, eight) : rt == 2 ? go(epi, two, eight) : go(epi, one, eight);
+    };
+    if (epilogue == PMN_EPI_SWIGLU) by_shape(std::integral_constant<int, PMN_EPI_SWIGLU>{});
+    else if (epilogue == PMN_EPI_F32) by_shape(std::integral_constant<int, PMN_EPI_F32>{});
+    else by_shape(std::integral_constant<int, PMN_EPI_BF16>{});
     return hipGetLastError();
 }
 

@@ -177,18 +177,11 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
                                  hipStream_t stream);
 
 int gemv_most_pairs();
-bool gemv_sums_at_once(int T, int k);
 // NVFP4 weights [G*N x K] times the rows of every pair of a token and an expert (x [T x K], per_pair: [T*k x K]):
 // out [T*k x N], SWIGLU [T*k x N/2]. ids null: matrix 0 (k = 1).
 hipError_t launch_gemv_pairs(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
                              const float* outer, int64_t rpo, const int32_t* ids, int T, int k, int G, int64_t N,
                              int64_t K, int epilogue, void* out, hipStream_t stream);
-// The pairs' sum with the gates (+ add) in one launch, where gemv_sums_at_once
-hipError_t launch_gemv_sum(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
-                           const float* outer, int64_t rpo, const int32_t* ids, const float* gates,
-                           const uint16_t* add, int T, int k, int G, int64_t N, int64_t K, bool f32, void* out,
-                           hipStream_t stream);
-
 // slot_of null: pair q is slot q; gates null: ones
 hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, const int32_t* slot_of,
                                const float* gates, const uint16_t* add, int64_t T, int k, void* out, bool out_f32,

@@ -93,7 +93,7 @@ def check(P, T, k, G, N, K, ids, per_pair, seed, per=None):
     (1, 1, 1, 32, 32), (1, 1, 1, 64, 7168), (1, 8, 48, 128, 1056), (1, 3, 3, 192, 96), (2, 4, 9, 64, 544),
     (5, 8, 16, 448, 2048), (15, 2, 40, 64, 160), (16, 16, 16, 64, 288), (17, 3, 4, 96, 1120), (33, 8, 12, 64, 384),
     (64, 8, 48, 128, 640), (61, 1, 1, 256, 512), (70, 2, 2, 64, 224), (130, 1, 1, 64, 128), (256, 16, 20, 64, 64),
-    (3, 20, 24, 64, 96), (40, 5, 300, 32, 64)])
+    (3, 20, 24, 64, 96), (40, 5, 300, 32, 64), (1, 2, 3, 64, 8224), (4, 1, 2, 64, 16480), (9, 2, 2, 32, 17280)])
 @pytest.mark.parametrize("per_pair", [False, True])
 def test_pairs_and_sums(P, T, k, G, N, K, per_pair):
     check(P, T, k, G, N, K, choose(T, k, G, T + k), per_pair, 7 * T + G + K)
@@ -152,14 +152,20 @@ def test_tokens_keep_to_themselves(P):
         assert torch.equal(a[~uses], b[~uses]) and torch.isnan(b[uses]).flatten(1).any(1).all()
 
 
-def test_one_column_does_not_depend_on_the_others(P):
-    """A token's rows are the same bits alone and in a batch of the same kernel."""
+@pytest.mark.parametrize("T", [2, 16, 40])
+def test_one_column_does_not_depend_on_the_others(P, T):
+    """A token's rows are the same bits whatever the other tokens' activations are, and as another token of the batch
+    (pairs of an expert are summed alike; how many there are chooses the instructions)."""
     G, N, K, k = 8, 128, 1056, 2
     wq = weights(P, G, N, K, 9)
-    x, ids = mk((16, K), 1.0, 10), choose(16, k, G, 11)
+    x, ids = mk((T, K), 1.0, 10), choose(T, k, G, 11)
     whole = P.moe_gemv_nvfp4(x, wq, N, ids, P.EPI_F32)
-    for t in (0, 7, 15):
-        assert torch.equal(P.moe_gemv_nvfp4(x[t:t + 1], wq, N, ids[t:t + 1], P.EPI_F32)[0], whole[t])
+    for t in (0, T // 2, T - 1):
+        other = mk((T, K), 1.0, 12)
+        other[t] = x[t]
+        assert torch.equal(P.moe_gemv_nvfp4(other, wq, N, ids, P.EPI_F32)[t], whole[t])
+    back = torch.arange(T - 1, -1, -1, device=DEV)
+    assert torch.equal(P.moe_gemv_nvfp4(x[back].contiguous(), wq, N, ids[back].contiguous(), P.EPI_F32)[back], whole)
 
 
 def test_memory_around_the_outputs(P):

@@ -58,8 +58,7 @@ def test_grouped_backward_refusals(lib):
 
 def test_gemv_refusals(lib):
     size = lib.moe_gemv_nvfp4_workspace_size
-    assert size(16, 16, 64, 1) == 0 and size(17, 2, 64, 0) == 0 and size(17, 2, 64, 1) >= 17 * 2 * 64 * 4
-    assert size(2, 17, 64, 1) >= 2 * 17 * 64 * 4
+    assert size(17, 2, 64, 0) == 0 and size(0, 2, 64, 1) == 0 and size(17, 2, 64, 1) >= 17 * 2 * 64 * 4
 
     def f(x=FAKE, pp=0, c=FAKE, s=FAKE, o=FAKE, rpo=64, ids=FAKE, gates=None, add=None, T=4, k=2, G=8, N=64, K=64, epi=1,
           out=FAKE, ws=None, nb=0):
@@ -76,7 +75,7 @@ def test_gemv_refusals(lib):
     assert f(T=20, gates=FAKE, ws=ODD, nb=size(20, 2, 64, 1)) == EALIGN
     for q in ("x", "c", "out"):
         assert f(**{q: ODD}) == EALIGN, q
-    assert f(gates=FAKE, add=ODD) == EALIGN and f(s=C.c_void_p(0x1002)) == EALIGN and f(ids=C.c_void_p(0x1002)) == EALIGN
+    assert f(gates=FAKE, add=ODD, ws=FAKE, nb=size(4, 2, 64, 1)) == EALIGN and f(s=ODD) == EALIGN and f(ids=C.c_void_p(0x1002)) == EALIGN
     assert f(T=0, x=None, out=None) == 0
 
 
