@@ -128,20 +128,11 @@ PMN_DEV void ffn_finish8(const FfnArgs& p, int64_t c, int64_t n, float (&v)[8], 
     }
 }
 
-// buffer descriptor of `bytes` bytes (at most 2^31 - 1) from p: loads past them return zero
-PMN_DEV i32x4 buffer_of(const void* p, int64_t bytes)
-{
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const int n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes);
-    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
-                 __builtin_amdgcn_readfirstlane(n), 0x00020000};
-}
-
-// 16 bytes per lane from buffer offset voff (past the buffer: zeros) to LDS lds + 16 lane. The
+// 16 bytes per lane from buffer offset voff + soff (voff past the buffer: zeros) to LDS lds + 16 lane. The
 // s_nop is the wait state that an LDS load needs after a write of m0.
-PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t lds)
+PMN_DEV void dma16_buffer(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory", "m0");
 }
 
@@ -245,7 +236,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             if (GATHER && !isr) {
                 from[i - T::RPW] = ok ? reinterpret_cast<const uint8_t*>(p.c + (int64_t)p.gather[c0 + t] * ld + s0 * 32 + ch * 8)
                                       : nullptr;
-                if (!ok) kch[i] = 32;   // past every stage
+                if (!ok) kch[i] = 0x7FFFFFFF;   // past every stage
             }
         } else {
             const int W = isr ? BR * 2 : BC * 2;                      // bytes of a stored row in the tile
@@ -258,59 +249,70 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
-    // An operand's bytes from its first at stage 0 of this part, a stage's advance and how many bytes
-    // there are. A k-contiguous operand is bounded by the lanes' row and chunk checks alone, which hold for
-    // this base and no other: its own byte count as a second bound took 10 to 30% of the forward, counted
-    // in 32 bits 1 to 4%.
-    struct Operand {
-        const uint8_t* base;
-        int64_t step, bytes;
-    };
-    auto operand = [&](const uint16_t* src, bool kc, int64_t ld, int64_t at) {
-        const int64_t k0 = s0 * 32;
-        Operand o;
-        o.base = reinterpret_cast<const uint8_t*>(kc ? src + at * ld + k0 : src + k0 * ld + at);
-        o.step = kc ? 64 : 64 * ld;
-        o.bytes = kc ? INT64_MAX : ((p.K - k0) * ld - at) * 2;
-        return o;
-    };
-    const Operand opr = operand(p.r, RKC, p.ldr, r0), opc = operand(p.c, CKC, p.ldc, c0);
-    const int64_t w3_bytes = SWI ? p.F * p.ldr * 2 : 0;
+    // A stage of this part: the operands' descriptors and how far it lies from the part's first. A
+    // k-contiguous operand's descriptor stays, its stage is the offset `at`; it is bounded by the lanes' row
+    // and chunk checks alone, which hold for its first row and no other (its own byte count as a second
+    // bound took 10 to 30% of the forward, counted in 32 bits 1 to 4%). A row-contiguous one's begins at the
+    // stage and ends with the contraction, or 32 rows past the stage.
+    const int kend = (int)(p.K < s1 * 32 ? p.K : s1 * 32);
+    const int64_t k0 = s0 * 32;
     struct Stage {
-        i32x4 r, r3, c;   // r3: the rows of w3
-        int left;         // k of this stage, at most 32; nothing is gathered past the part's last stage
-        int64_t at;       // its bytes from the part's first (GATHER)
+        uint64_t r, c;    // first bytes
+        int rrec, crec;   // and bytes from there
+        uint32_t at;
+        int left;         // k from the stage's first to the part's end: none where it is not positive
         uint32_t dst;
+    };
+    const uint64_t r3 = SWI ? (uint64_t)p.F * p.ldr * 2 : 0;   // from w1's rows to w3's
+    constexpr bool ONE_HALF = SWI && !ROTATE && RB % T::RPW == 0;   // a wavefront's pieces of R are all of w1 or all of w3
+    auto of_w3 = [&](int i) { return SWI && (piece_of(i) >> 1) % RB >= RB / 2; };
+    auto records = [&](int left, int64_t ld, int64_t at) {
+        const int rows = left < 64 ? left : 64;
+        return rows > 0 ? (int)((rows * (int)ld - (int)at) * 2) : 0;
     };
     auto stage_at = [&](int s) {
         Stage g;
-        const bool in = s < nst;   // nothing past the part's last stage
-        g.r = buffer_of(opr.base + s * opr.step, in ? opr.bytes - s * opr.step : 0);
-        if (SWI) g.r3 = buffer_of(opr.base + w3_bytes + s * opr.step, in ? opr.bytes - s * opr.step : 0);
-        if (!GATHER) g.c = buffer_of(opc.base + s * opc.step, in ? opc.bytes - s * opc.step : 0);
-        g.at = (int64_t)s * 64;
-        const int64_t left = GATHER && !in ? 0 : p.K - (s0 + s) * 32;
-        g.left = left > 32 ? 32 : (int)left;
-        g.dst = (uint32_t)(s % NST) * T::STAGE;
+        g.r = reinterpret_cast<uint64_t>(RKC ? p.r + r0 * p.ldr + k0 : p.r + (k0 + (int64_t)s * 32) * p.ldr + r0);
+        if (ONE_HALF && of_w3(0)) g.r += r3;
+        g.c = reinterpret_cast<uint64_t>(CKC ? p.c + c0 * p.ldc + k0 : p.c + (k0 + (int64_t)s * 32) * p.ldc + c0);
+        g.at = (uint32_t)s * 64;
+        g.left = kend - (int)k0 - s * 32;
+        g.rrec = RKC ? 0x7FFFFFFF : records(g.left, p.ldr, r0);
+        g.crec = CKC ? 0x7FFFFFFF : records(g.left, p.ldc, c0);
+        g.dst = (uint32_t)(s % NST) * T::STAGE + lds0;
         return g;
     };
-    auto issue_piece = [&](const Stage& g, int i) {
+    // the same `by` stages on; in scalar instructions few enough for the gap between two MFMAs
+    auto advance = [&](Stage& g, auto by) {
+        constexpr int BY = decltype(by)::value;
+        g.left -= 32 * BY;
+        g.at += 64 * BY;
+        g.dst += BY * T::STAGE;
+        g.dst = g.dst >= lds0 + NST * T::STAGE ? g.dst - NST * T::STAGE : g.dst;
+        if (!RKC) {
+            g.r += (uint64_t)(64 * BY) * p.ldr;
+            g.rrec = records(g.left, p.ldr, r0);
+        }
+        if (!CKC) {
+            g.c += (uint64_t)(64 * BY) * p.ldc;
+            g.crec = records(g.left, p.ldc, c0);
+        }
+    };
+    auto descriptor = [](uint64_t first, int bytes) {
+        return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)first), __builtin_amdgcn_readfirstlane((int)(uint32_t)(first >> 32)),
+                     __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+    };
+    // Piece i's lane offset in stage g: chunks past the part's end of a k-contiguous operand lie outside
+    auto lane_offset = [&](const Stage& g, int i) { return (i < T::RPW ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i]; };
+    auto issue_piece = [&](const Stage& g, int i, uint32_t v) {
         const bool isr = i < T::RPW;
-        // chunks past K of a k-contiguous operand
-        const uint32_t v = (isr ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i];
         if (GATHER && !isr) {
             const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
-            dma16_flat(kch[i] >= g.left ? z : from[i - T::RPW] + g.at, g.dst + lds0 + T::RBYTES + piece_of(i) * 1024);
+            dma16_flat(kch[i] >= g.left ? z : from[i - T::RPW] + g.at, g.dst + T::RBYTES + piece_of(i) * 1024);
         } else if (!isr) {
-            dma16_buffer(g.c, v, g.dst + lds0 + T::RBYTES + piece_of(i) * 1024);
-        } else if (!SWI) {
-            dma16_buffer(g.r, v, g.dst + lds0 + piece_of(i) * 1024);
+            dma16_buffer(descriptor(g.c, g.crec), v, CKC ? g.at : 0u, g.dst + T::RBYTES + piece_of(i) * 1024);
         } else {
-            const bool w3 = (piece_of(i) >> 1) % RB >= RB / 2;
-            i32x4 d;
-#pragma unroll
-            for (int q = 0; q < 4; q++) d[q] = __builtin_amdgcn_readfirstlane(w3 ? g.r3[q] : g.r[q]);
-            dma16_buffer(d, v, g.dst + lds0 + piece_of(i) * 1024);
+            dma16_buffer(descriptor(!ONE_HALF && of_w3(i) ? g.r + r3 : g.r, g.rrec), v, RKC ? g.at : 0u, g.dst + piece_of(i) * 1024);
         }
     };
 
@@ -347,20 +349,33 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // The MFMAs of a step with its PPW loads spread over them and the fragment reads of stage `next`
-    // over the first three quarters, so that the last have come back before the next step's barrier
-    // (all loads before all reads measured 4% slower).
+    // The MFMAs of a step, each followed by what fits next to it (a wavefront has a SIMD to itself in the
+    // 256 x 256 tiles and issues one instruction in 4 cycles, 7 next to an MFMA): its PPW loads spread over the
+    // step, each with its lane offset ready one MFMA earlier; the fragment reads of stage `next` in the other
+    // places of the first three quarters, so that the last have come back before the next step's barrier;
+    // the next stages' scalars (other) at the end.
     constexpr int NM = 2 * RB * CB, NRQ = NM * 3 / 4;
-    auto compute = [&](int next, const Frags& cur, Frags& nxt, auto load) {
+    constexpr bool ROOMY = NM >= 2 * (NREAD / 2 + PPW);   // loads and reads have places of their own
+    auto load_of = [](int q) { return (q + 1) * PPW / NM > q * PPW / NM ? q * PPW / NM : -1; };   // at most one a place where ROOMY
+    auto compute = [&](int next, const Frags& cur, Frags& nxt, auto ready, auto load, auto other) {
         const uint8_t* rbase = lds + (next % NST) * T::STAGE;
+        int read = 0;
+        uint32_t v[PPW];
 #pragma unroll
         for (int q = 0; q < NM; q++) {
             const int ks = q / (RB * CB), i = (q / CB) % RB, j = q % CB;
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cur.r[i][ks], cur.c[j][ks], acc[i][j], 0, 0, 0);
+            if constexpr (ROOMY) {
+                if (q + 1 < NM && load_of(q + 1) >= 0) v[load_of(q + 1)] = ready(load_of(q + 1));
+                if (load_of(q) >= 0) load(load_of(q), v[load_of(q)]);
+                else if (read < NREAD) read_one(rbase, read++, nxt);
+            } else {
 #pragma unroll
-            for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
+                for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
 #pragma unroll
-            for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) load(n);
+                for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) load(n, ready(n));
+            }
+            other(q);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -369,20 +384,25 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 #pragma unroll
         for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
     };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    constexpr int LATE = NM * 3 / 4;   // where the next stages' scalars are formed
     if constexpr (!PAIRED) {
+        Stage g = stage_at(0);
 #pragma unroll
         for (int s = 0; s < NST; s++) {
-            const Stage g = stage_at(s);
 #pragma unroll
-            for (int i = 0; i < PPW; i++) issue_piece(g, i);
+            for (int i = 0; i < PPW; i++) issue_piece(g, i, lane_offset(g, i));
+            advance(g, one);
         }
         wait_loads_and_barrier<(NST - 1) * PPW>();
         read_first();
         // stage v + 1 has landed and every wavefront is done reading stage v, whose slot is refilled
         auto step = [&](int v, const Frags& cur, Frags& nxt) {
             wait_loads_and_barrier<(NST - 2) * PPW>();
-            const Stage g = stage_at(v + NST);
-            compute(v + 1, cur, nxt, [&](int n) { issue_piece(g, n); });
+            const Stage h = g;   // stage v + NST
+            compute(v + 1, cur, nxt, [&](int n) { return lane_offset(h, n); }, [&](int n, uint32_t o) { issue_piece(h, n, o); },
+                    [&](int q) { if (q == LATE) advance(g, one); });
         };
         for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
             step(v, f0, f1);
@@ -394,30 +414,37 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         // of its lines is in the first-level cache (8192 x 7168 x 2048 forward: 707 us with single stages,
         // 660 in pairs; row-contiguous operands, whose stages are whole lines, lose 5% by it). Slots of
         // stages v - 1 and v are free at step v; half of the pieces are loaded then, half at step v + 1.
+        Stage g0 = stage_at(0), g1 = stage_at(1);
 #pragma unroll
         for (int s = 0; s < NST - 1; s += 2) {
-            const Stage g0 = stage_at(s), g1 = stage_at(s + 1);
 #pragma unroll
             for (int i = 0; i < PPW; i++) {
-                issue_piece(g0, i);
-                issue_piece(g1, i);
+                issue_piece(g0, i, lane_offset(g0, i));
+                issue_piece(g1, i, lane_offset(g1, i));
             }
+            advance(g0, two);
+            advance(g1, two);
         }
         wait_loads_and_barrier<(NST - 3) * PPW>();
         read_first();
-        auto step = [&](int v, int odd, const Frags& cur, Frags& nxt) {
-            const Stage g0 = stage_at(v + NST - 1), g1 = stage_at(v + NST);
-            compute(v + odd + 1, cur, nxt, [&](int n) {
+        auto step = [&](int v, auto second, const Frags& cur, Frags& nxt) {
+            constexpr int odd = decltype(second)::value ? 1 : 0;
+            auto piece = [&](int n) {
                 const bool isr = n < T::RPW;
                 const int m = isr ? n : n - T::RPW, half = (isr ? T::RPW : T::CPW) / 2;
-                issue_piece(m & 1 ? g1 : g0, (isr ? 0 : T::RPW) + odd * half + (m >> 1));
-            });
+                return (isr ? 0 : T::RPW) + odd * half + (m >> 1);
+            };
+            auto stage = [&](int n) -> const Stage& { return ((n < T::RPW ? n : n - T::RPW) & 1) ? g1 : g0; };
+            compute(v + odd + 1, cur, nxt, [&](int n) { return lane_offset(stage(n), piece(n)); },
+                    [&](int n, uint32_t o) { issue_piece(stage(n), piece(n), o); }, [](int) {});
         };
         for (int v = 0; v < nst; v += 2) {
             wait_loads_and_barrier<63>();      // stage v + 1 landed with its pair
-            step(v, 0, f0, f1);
+            step(v, std::false_type{}, f0, f1);
             wait_loads_and_barrier<PPW>();     // the pair v + 2, v + 3: all but step v's loads
-            step(v, 1, f1, f0);
+            step(v, std::true_type{}, f1, f0);
+            advance(g0, two);
+            advance(g1, two);
         }
     }
     wait_loads_and_barrier<0>();

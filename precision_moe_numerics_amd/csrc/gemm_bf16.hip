@@ -201,11 +201,51 @@ typedef FfnTile<2, 2, 4, 4, 4> GroupLarge;   // 256 x 256, one workgroup per CU
 typedef FfnTile<2, 2, 2, 2, 4> GroupMid;     // 128 x 128
 typedef FfnTile<2, 2, 2, 1, 4> GroupSlim;    // 128 x 64
 
-// Tile by the mean slots of a group: 0 large, 1 mid, 2 slim, 3 sixteen slots (k-contiguous weights)
-static int group_plan(int64_t M, int G, bool rkc)
+// Tiles and their times of one round of 256 workgroups, in us of a contraction of 4096 plus what a tile
+// takes beside it (first loads, epilogue), taken from 60 sizes of 1 to 48 groups; half: a large tile of at most
+// 128 slots, as nearly all are where the groups' mean is that small.
+struct GroupTile {
+    int br, bc;
+    double full, half, rest;
+};
+enum { GROUP_LARGE = 0, GROUP_MID = 1, GROUP_SLIM = 2, GROUP_FEW = 3 };
+static const GroupTile GROUP_TILES[4] = {{256, 256, 80.0, 49.0, 14.0}, {128, 128, 36.0, 36.0, 2.0},
+                                         {128, 64, 28.0, 28.0, 2.0}, {16, 16, 6.3, 6.3, 1.0}};
+
+// The tile whose rounds are shortest for a product of `rows` rows of R (contraction K) over M slots of G
+// groups. The choice follows from the host's sizes: units that the groups end in are taken as half a one
+// each. (us, large / mid / slim / few: 480 slots in 48 groups of 4096 x 7168 473 / 486 / 497 / 665; 1024 in
+// 4 of 4096 x 4096 80 / 62 / 80 / 480; 16 in 4 of 1024 x 7168 76 / 53 / 40 / 13. At most 16% from the best of
+// the four where it errs: 64 slots of 16 x 4096 x 4096 111 against 133 were it the large one.)
+static int group_plan(int64_t M, int G, int64_t rows, int64_t K, bool rkc)
 {
-    const int64_t mean = M / G;
-    return mean > 160 ? 0 : mean > 64 ? 1 : mean > 16 || !rkc ? 2 : 3;
+    const double some = (double)(M < G ? M : G);   // groups with slots, at most
+    int best = GROUP_LARGE;
+    double least = 0.0;
+    for (int i = 0; i < (rkc ? 4 : 3); i++) {
+        const GroupTile& t = GROUP_TILES[i];
+        const double full = (double)M / t.bc + some / 2.0, units = full > some ? full : some;
+        double rounds = units * (double)((rows + t.br - 1) / t.br) / 256.0;
+        if (rounds <= 2.0) rounds = rounds <= 1.0 ? 1.0 : i == GROUP_MID ? rounds : 2.0;   // two mid tiles fit a CU side by side
+        const double us = rounds * ((M <= 128 * some ? t.half : t.full) * (double)K / 4096.0 + t.rest);
+        if (i == 0 || us < least) {
+            best = i;
+            least = us;
+        }
+    }
+    return best;
+}
+
+// dW's tile: 256 x 256 (us of its rest beside the contraction: 8) or 128 x 128. (32 groups of 2048 x 4096,
+// bf16: 512 slots 125 / 130, 8192 210 / 234, 131072 in fp32 1.76 / 2.1 ms; fewer than 256 large tiles leave CUs idle.)
+static bool wgrad_large(int64_t M, int G, int64_t N, int64_t K)
+{
+    const double k = (double)M / G / 4096.0;
+    auto us = [&](int b, double t, double rest) {
+        const double rounds = (double)G * (double)((N + b - 1) / b) * (double)((K + b - 1) / b) / 256.0;
+        return (rounds < 1.0 ? 1.0 : rounds) * (t * k + rest);
+    };
+    return us(256, 80.0, 8.0) <= us(128, 36.0, 2.0);
 }
 
 // Workgroups of a product over the slots: rows of R in tiles of br, slots in units (a group adds at
@@ -225,12 +265,10 @@ static int64_t wgrad_grid(int G, int64_t N, int64_t K, int64_t b)
 bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd)
 {
     const int64_t most = ((int64_t)1 << 32) - 1;
-    const int plan = group_plan(M, G, fwd);
-    const int64_t rows = fwd ? N : K;
-    const int64_t br[4] = {256, 128, 128, 16}, unit[4] = {256, 128, 64, 16};
+    const GroupTile& t = GROUP_TILES[group_plan(M, G, fwd ? N : K, fwd ? K : N, fwd)];
     // (SwiGLU's F features in tiles of half as many are at most one tile of R more)
-    if ((group_grid(M, G, rows, br[plan], unit[plan]) + (M / unit[plan] + G)) > most / (plan == 3 ? 512 : 256)) return false;
-    return fwd || wgrad_grid(G, N, K, plan == 0 ? 256 : 128) <= most / 256;
+    if (group_grid(M, G, fwd ? N : K, t.br, t.bc) + (M / t.bc + G) > most / (t.bc == 16 ? 512 : 256)) return false;
+    return fwd || wgrad_grid(G, N, K, wgrad_large(M, G, N, K) ? 256 : 128) <= most / 256;
 }
 
 template <typename T, bool RKC, int EPI, bool GATHER>
@@ -245,9 +283,9 @@ static void group_launch(GroupArgs a, int64_t M, hipStream_t stream)
 template <bool RKC, int EPI, bool GATHER>
 static void group_gemm(const GroupArgs& a, int64_t M, hipStream_t stream)
 {
-    const int plan = group_plan(M, a.G, RKC);
+    const int plan = group_plan(M, a.G, a.p.Nr, a.p.K, RKC);
     if constexpr (RKC) {
-        if (plan == 3) {
+        if (plan == GROUP_FEW) {
             GroupArgs b = a;
             const int64_t nr = EPI == FFN_SWIGLU ? a.p.F : a.p.Nr, br = EPI == FFN_SWIGLU ? 8 : 16;
             b.p.rtiles = (nr + br - 1) / br;
@@ -255,8 +293,8 @@ static void group_gemm(const GroupArgs& a, int64_t M, hipStream_t stream)
             return;
         }
     }
-    if (plan == 0) group_launch<GroupLarge, RKC, EPI, GATHER>(a, M, stream);
-    else if (plan == 1) group_launch<GroupMid, RKC, EPI, GATHER>(a, M, stream);
+    if (plan == GROUP_LARGE) group_launch<GroupLarge, RKC, EPI, GATHER>(a, M, stream);
+    else if (plan == GROUP_MID) group_launch<GroupMid, RKC, EPI, GATHER>(a, M, stream);
     else group_launch<GroupSlim, RKC, EPI, GATHER>(a, M, stream);
 }
 
@@ -320,7 +358,7 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
         };
         typedef std::integral_constant<int, FFN_F32> F32;
         typedef std::integral_constant<int, FFN_BF16> BF16;
-        if (group_plan(M, G, false) == 0) {
+        if (wgrad_large(M, G, N, K)) {
             if (dw_f32) run(GroupLarge{}, F32{});
             else run(GroupLarge{}, BF16{});
         } else {

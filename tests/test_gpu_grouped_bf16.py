@@ -92,7 +92,11 @@ CASES = [([1], 32, 64, 0), ([0, 3, 0, 16, 17, 0], 48, 72, 0), ([5, 0, 0, 1], 264
          ([33, 0, 64, 65, 1], 144, 264, 0), ([40, 20, 90, 0], 520, 328, 77), ([100, 128, 129, 64], 272, 136, 0),
          ([130, 0, 127, 1, 200], 136, 520, 300), ([256, 257, 128, 385, 0, 300], 528, 264, 0),
          ([700, 3, 511], 256, 96, 0), ([300, 129, 384, 640], 784, 1032, 500), ([1025], 264, 2056, 0),
-         ([0] * 66 + [20], 64, 64, 0), ([9, 14, 3, 30], 1040, 4104, 21)]
+         ([0] * 66 + [20], 64, 64, 0), ([9, 14, 3, 30], 1040, 4104, 21),
+         # enough tiles of a long contraction for the 256 x 256 ones, whole and half, and for 128 x 128 ones
+         ([4000, 0, 129, 2500, 1, 1250, 1120], 1040, 4104, 0), ([3000, 128, 0, 1500, 257, 4115], 1040, 4104, 2000),
+         ([(i * 37) % 125 for i in range(48)], 1040, 4104, 700), ([300 + (i * 61) % 97 for i in range(40)], 784, 1032, 0),
+         ([2600, 5, 1400], 2064, 520, 900)]
 IDS = [f"{len(c[0])}x{sum(c[0])}-{c[1]}x{c[2]}-{c[3]}" for c in CASES]
 
 
