@@ -843,8 +843,8 @@ def moe_grouped_gemm_fwd_bf16(x: torch.Tensor, w: torch.Tensor, offsets: torch.T
     return (out, out_aux) if swiglu else out
 
 
-def moe_grouped_gemm_bwd_bf16_workspace_size(M: int, K: int, flags: int, own_rows: bool) -> int:
-    return _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(own_rows))
+def moe_grouped_gemm_bwd_bf16_workspace_size(M: int, K: int, flags: int, from_h13: bool) -> int:
+    return _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(from_h13))
 
 
 def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor, offsets: torch.Tensor,
@@ -880,7 +880,7 @@ def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: to
         _tensor(db, (G * N, K), db_dtype, "db")
     elif wgrad:
         db = torch.empty((G * N, K), dtype=db_dtype, device=dev)
-    need = _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(gather is not None or x is None))
+    need = _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, 1) if x is None else 0
     workspace = _workspace(workspace, need, dev) if need or workspace is not None else None
     _check(_lib.moe_grouped_gemm_bwd_bf16(
         _device_ptr(dy, at, "dy"), _device_ptr(x, at, "x"), 0 if x is None else x.shape[0],

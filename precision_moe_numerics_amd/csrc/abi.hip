@@ -599,9 +599,9 @@ int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gath
                                              hs(stream)));
 }
 
-size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int own_rows)
+size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int from_h13)
 {
-    return M <= 0 || K <= 0 || !(flags & PMN_BWD_WGRAD) || !own_rows ? 0 : round256((size_t)(M * K) * 2);
+    return M <= 0 || K <= 0 || !(flags & PMN_BWD_WGRAD) || !from_h13 ? 0 : round256((size_t)(M * K) * 2);
 }
 
 int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, const int32_t* gather, const void* w,
@@ -620,19 +620,18 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
     const bool rebuild = wgrad && !x && h13;
     if (!offsets || (wgrad && !db)) return PMN_EINVAL;
     if (M > 0 && (!dy || (dgrad && (!w || !da)) || (wgrad && !x && !rebuild))) return PMN_EINVAL;
-    const size_t need = moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, gather != nullptr || rebuild);
+    const size_t need = moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, rebuild);
     if (need > 0 && (!workspace || workspace_bytes < need)) return PMN_EWORKSPACE;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(h13, 16) || !aligned(gather, 4) ||
         !aligned(offsets, 8) || (dgrad && !aligned(da, 16)) || (wgrad && !aligned(db, 16)) ||
         (need > 0 && !aligned(workspace, 16)))
         return PMN_EALIGN;
     if (M == 0 && !wgrad) return PMN_OK;
-    uint16_t* const rows = need > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
+    uint16_t* const act = rebuild ? static_cast<uint16_t*>(workspace) : nullptr;
     return status(pmn::launch_group_bwd_bf16(
-        static_cast<const uint16_t*>(dy), rebuild ? rows : static_cast<const uint16_t*>(x), gather,
+        static_cast<const uint16_t*>(dy), rebuild ? act : static_cast<const uint16_t*>(x), gather,
         static_cast<const uint16_t*>(w), offsets, G, M, N, K, static_cast<const uint16_t*>(h13), dgrad ? da : nullptr,
-        da_dtype == PMN_DTYPE_F32, rebuild ? rows : nullptr, rows, wgrad ? db : nullptr, db_dtype == PMN_DTYPE_F32,
-        hs(stream)));
+        da_dtype == PMN_DTYPE_F32, act, wgrad ? db : nullptr, db_dtype == PMN_DTYPE_F32, hs(stream)));
 }
 
 static bool bad_gemv_shape(int64_t T, int k, int G, int64_t N, int64_t K)

@@ -49,8 +49,9 @@ struct FfnArgs {
     int splits;
     int64_t rtiles, ctiles;
     int64_t whole;          // tiles that run whole; the others in two halves (ffn_grid)
-    const int32_t* gather;  // GATHER: the stored row of C that each of its rows is
+    const int32_t* gather;  // GATHER: the stored row that each row of C, or each k of R, is
 };
+enum { GATHER_NONE = 0, GATHER_C = 1, GATHER_R = 2 };
 
 // The 16-byte words of aux that 8 consecutive outputs n .. n+7 of output row c need: ADD's add, or
 // SWIGLU_BWD's h1 and h3.
@@ -161,7 +162,7 @@ struct FfnTile {
     static constexpr int RING = (PAIRS ? 5 : NST) * STAGE, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
-    static_assert((PAIRS ? 6 : NST - 1) * PPW <= 63, "vmcnt");
+    static_assert((PAIRS ? 6 : NST - 1) * (PPW + 1) <= 63, "vmcnt");
 };
 
 // Item number of workgroup L among n: workgroups L, L + 8, .. run on one XCD and take consecutive items.
@@ -182,16 +183,27 @@ PMN_DEV void ffn_tile_at(const FfnArgs& p, int64_t i, int64_t& trow, int64_t& tc
     trow = band * 8 + (in - tcol * height);
 }
 
-// The tile (trow, tcol) of a product, or part `split` of its contraction (PART). GATHER: row i of C
-// (k-contiguous) is stored row gather[i] of c.
-template <typename T, bool RKC, bool CKC, int EPI, bool GATHER = false>
+// 4 bytes per lane to LDS lds + 4 lane
+PMN_DEV void dma4_flat(const void* src, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+
+// The tile (trow, tcol) of a product, or part `split` of its contraction (PART). GATHER_C: row i of C
+// (k-contiguous) is stored row gather[i] of c. GATHER_R: k of R (row-contiguous) is stored row gather[k] of r.
+template <typename T, bool RKC, bool CKC, int EPI, int GATHER = GATHER_NONE>
 PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, uint8_t* lds)
 {
     constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, PPW = T::PPW;
     constexpr bool SWI = EPI == FFN_SWIGLU, PAIRED = T::PAIRS && RKC && CKC;
     constexpr int NST = PAIRED ? 5 : T::NST;
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
-    static_assert(!GATHER || CKC, "rows are gathered of a k-contiguous operand");
+    static_assert(GATHER != GATHER_C || CKC, "C's rows are gathered where it is k-contiguous");
+    static_assert(GATHER != GATHER_R || (!RKC && !CKC && EPI != FFN_PART), "R's k are gathered where it is row-contiguous, in wgrad");
+    // GATHER_R: the indices of a wavefront's rows of a stage, loaded 8 stages ahead into 8 slots behind the ring
+    constexpr int ROWS = 512 / BR, SLOTS = 8, SLOT = 256;   // stored rows of a piece of R
+    static_assert(GATHER != GATHER_R || (NST == 4 && T::RPW * ROWS == 8 && NST * T::STAGE + T::WR * T::WC * SLOTS * SLOT <= T::LDS), "index slots");
+    constexpr int LPS = PPW + (GATHER == GATHER_R ? 1 : 0);   // loads of a stage and wavefront
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / T::WC, wc = wave % T::WC, l32 = lane & 31, hh = lane >> 5;
@@ -213,7 +225,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     };
     uint32_t voff[PPW];
     int kch[PPW];
-    const uint8_t* from[GATHER ? T::CPW : 1];   // the gathered rows' chunks at this part's first stage
+    const uint8_t* from[GATHER == GATHER_C ? T::CPW : 1];   // the gathered rows' chunks at this part's first stage
 #pragma unroll
     for (int i = 0; i < PPW; i++) {
         const bool isr = i < T::RPW;
@@ -233,7 +245,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             }
             voff[i] = ok ? (uint32_t)(row * ld * 2 + ch * 16) : FFN_OUTSIDE;
             kch[i] = ch * 8;
-            if (GATHER && !isr) {
+            if (GATHER == GATHER_C && !isr) {
                 from[i - T::RPW] = ok ? reinterpret_cast<const uint8_t*>(p.c + (int64_t)p.gather[c0 + t] * ld + s0 * 32 + ch * 8)
                                       : nullptr;
                 if (!ok) kch[i] = 0x7FFFFFFF;   // past every stage
@@ -246,6 +258,10 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             const bool ok = (isr ? r0 : c0) + col < (isr ? p.Nr : p.Nc);
             voff[i] = ok ? (uint32_t)(k * ld * 2 + col * 2) : FFN_OUTSIDE;
             kch[i] = 0;
+            if (GATHER == GATHER_R && isr) {
+                voff[i] = col * 2;              // within a stored row
+                kch[i] = ok ? k : 0x7FFFFFFF;   // the lane's k of the stage
+            }
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
@@ -272,7 +288,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     };
     auto stage_at = [&](int s) {
         Stage g;
-        g.r = reinterpret_cast<uint64_t>(RKC ? p.r + r0 * p.ldr + k0 : p.r + (k0 + (int64_t)s * 32) * p.ldr + r0);
+        g.r = GATHER == GATHER_R ? 0 : reinterpret_cast<uint64_t>(RKC ? p.r + r0 * p.ldr + k0 : p.r + (k0 + (int64_t)s * 32) * p.ldr + r0);
         if (ONE_HALF && of_w3(0)) g.r += r3;
         g.c = reinterpret_cast<uint64_t>(CKC ? p.c + c0 * p.ldc + k0 : p.c + (k0 + (int64_t)s * 32) * p.ldc + c0);
         g.at = (uint32_t)s * 64;
@@ -289,7 +305,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         g.at += 64 * BY;
         g.dst += BY * T::STAGE;
         g.dst = g.dst >= lds0 + NST * T::STAGE ? g.dst - NST * T::STAGE : g.dst;
-        if (!RKC) {
+        if (!RKC && GATHER != GATHER_R) {
             g.r += (uint64_t)(64 * BY) * p.ldr;
             g.rrec = records(g.left, p.ldr, r0);
         }
@@ -304,9 +320,33 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     };
     // Piece i's lane offset in stage g: chunks past the part's end of a k-contiguous operand lie outside
     auto lane_offset = [&](const Stage& g, int i) { return (i < T::RPW ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i]; };
+    struct Index {
+        uint32_t v[GATHER == GATHER_R ? T::RPW : 1];
+    };
+    Index index;   // stored rows of this wavefront's pieces of R of the stage that is loaded next
+    const int sub = (lane * 16) / (BR * 2);   // the lane's row of a piece
+    const int64_t last = p.K > 0 ? p.K - 1 : 0;
+    auto index_at = [&](int64_t k) { return p.K > 0 ? p.gather + (k < last ? k : last) : reinterpret_cast<const int32_t*>(&ffn_zeros); };
+    const uint32_t slot0 = lds0 + NST * T::STAGE + wave * (SLOTS * SLOT);
+    auto load_index = [&](int s) {   // lane e (of 8) of each 8: row e / RPW of piece e % RPW
+        const int e = lane & 7;
+        const int piece = (wave * T::RPW + e % T::RPW + rotr) % (BR / 16);
+        dma4_flat(index_at((int64_t)s * 32 + piece * ROWS + e / T::RPW), slot0 + (s & (SLOTS - 1)) * SLOT);
+    };
+    auto read_index = [&](int s) {
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(lds + NST * T::STAGE + wave * (SLOTS * SLOT) + (s & (SLOTS - 1)) * SLOT) + sub * T::RPW;
+        Index x;
+#pragma unroll
+        for (int i = 0; i < T::RPW; i++) x.v[GATHER == GATHER_R ? i : 0] = a[i];
+        return x;
+    };
     auto issue_piece = [&](const Stage& g, int i, uint32_t v) {
         const bool isr = i < T::RPW;
-        if (GATHER && !isr) {
+        if (GATHER == GATHER_R && isr) {
+            const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
+            const uint8_t* row = reinterpret_cast<const uint8_t*>(p.r + r0) + (uint64_t)index.v[i] * (uint64_t)(uint32_t)(p.ldr * 2) + voff[i];
+            dma16_flat(kch[i] >= g.left ? z : row, g.dst + piece_of(i) * 1024);
+        } else if (GATHER == GATHER_C && !isr) {
             const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
             dma16_flat(kch[i] >= g.left ? z : from[i - T::RPW] + g.at, g.dst + T::RBYTES + piece_of(i) * 1024);
         } else if (!isr) {
@@ -389,20 +429,44 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     constexpr int LATE = NM * 3 / 4;   // where the next stages' scalars are formed
     if constexpr (!PAIRED) {
         Stage g = stage_at(0);
+        if constexpr (GATHER == GATHER_R) {
+            Index at[NST];
 #pragma unroll
-        for (int s = 0; s < NST; s++) {
+            for (int s = 0; s < NST; s++)
 #pragma unroll
-            for (int i = 0; i < PPW; i++) issue_piece(g, i, lane_offset(g, i));
-            advance(g, one);
+                for (int i = 0; i < T::RPW; i++) at[s].v[i] = (uint32_t)*index_at(s * 32 + piece_of(i) * ROWS + sub);
+#pragma unroll
+            for (int s = 0; s < NST; s++) {
+                index = at[s];
+#pragma unroll
+                for (int i = 0; i < PPW; i++) issue_piece(g, i, lane_offset(g, i));
+                load_index(s + NST);
+                advance(g, one);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NST; s++) {
+#pragma unroll
+                for (int i = 0; i < PPW; i++) issue_piece(g, i, lane_offset(g, i));
+                advance(g, one);
+            }
         }
-        wait_loads_and_barrier<(NST - 1) * PPW>();
+        wait_loads_and_barrier<(NST - 1) * LPS>();
         read_first();
+        if constexpr (GATHER == GATHER_R) index = read_index(NST);
         // stage v + 1 has landed and every wavefront is done reading stage v, whose slot is refilled
         auto step = [&](int v, const Frags& cur, Frags& nxt) {
-            wait_loads_and_barrier<(NST - 2) * PPW>();
+            wait_loads_and_barrier<(NST - 2) * LPS>();
             const Stage h = g;   // stage v + NST
+            Index ahead;
+            if constexpr (GATHER == GATHER_R) ahead = read_index(v + NST + 1);
             compute(v + 1, cur, nxt, [&](int n) { return lane_offset(h, n); }, [&](int n, uint32_t o) { issue_piece(h, n, o); },
-                    [&](int q) { if (q == LATE) advance(g, one); });
+                    [&](int q) {
+                        if (q == LATE) advance(g, one);
+                        if constexpr (GATHER == GATHER_R)
+                            if (q == LATE + 1) load_index(v + 2 * NST);
+                    });
+            if constexpr (GATHER == GATHER_R) index = ahead;
         };
         for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
             step(v, f0, f1);
@@ -499,6 +563,19 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         for (int k = 0; k < NP; k++) {
             int rr, n;
             int64_t c;
+            if constexpr (EPI == FFN_F32) {
+                // 4 values of each half of the tile's row: whole 128-byte lines of a row at a store
+                typedef float f32x4u __attribute__((ext_vector_type(4)));
+                place(j, k, rr, n, c);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int m = h * (BR / 2) + n / 2;
+                    if (c < p.Nc && r0 + m < p.Nr)
+                        __builtin_nontemporal_store(*reinterpret_cast<const f32x4u*>(ot + rr * T::OPITCH + m),
+                                                    reinterpret_cast<f32x4u*>(static_cast<float*>(p.out) + c * p.Nr + r0 + m));
+                }
+                continue;
+            }
             if (!place(j, k, rr, n, c)) continue;
             const float* src = ot + rr * T::OPITCH + n;
             float v[8], v2[8];

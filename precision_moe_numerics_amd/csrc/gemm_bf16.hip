@@ -84,16 +84,16 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_gro
     if (!group_tile<GATHER>(a, blockIdx.x, T::BC, p, trow, tcol)) return;
     if constexpr (T::HALVES) {
         if (p.Nc - tcol * T::BC <= T::BC / 2) {
-            ffn_tile<typename T::Half, RKC, true, EPI, GATHER>(p, trow, 2 * tcol, 0, lds);
+            ffn_tile<typename T::Half, RKC, true, EPI, GATHER ? GATHER_C : GATHER_NONE>(p, trow, 2 * tcol, 0, lds);
             return;
         }
     }
-    ffn_tile<T, RKC, true, EPI, GATHER>(p, trow, tcol, 0, lds);
+    ffn_tile<T, RKC, true, EPI, GATHER ? GATHER_C : GATHER_NONE>(p, trow, tcol, 0, lds);
 }
 
 // dW: p.Nr = K columns, p.Nc = N rows, contraction over the group's slots. The tiles of each group are
 // dealt to all XCDs in runs, as the groups differ in length.
-template <typename T, int EPI>
+template <typename T, int EPI, bool GATHER>
 __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_group_wgrad(GroupArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
@@ -103,13 +103,14 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_gro
     if (i >= tiles || g >= a.G) return;
     const int64_t s0 = uniform64(a.offsets[g]), s1 = uniform64(a.offsets[g + 1]);
     FfnArgs p = a.p;
-    p.r += s0 * p.ldr;
+    if (GATHER) p.gather += s0;
+    else p.r += s0 * p.ldr;
     p.c += s0 * p.ldc;
     p.K = s1 - s0;
     p.out = static_cast<uint8_t*>(p.out) + g * p.Nc * p.Nr * a.out_bytes;
     int64_t trow, tcol;
     ffn_tile_at(p, i, trow, tcol);
-    ffn_tile<T, false, false, EPI>(p, trow, tcol, 0, lds);
+    ffn_tile<T, false, false, EPI, GATHER ? GATHER_R : GATHER_NONE>(p, trow, tcol, 0, lds);
 }
 
 // Forward for few slots a group: units of 16 slots, the weights straight to registers. A workgroup holds
@@ -318,21 +319,10 @@ hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const
     return hipGetLastError();
 }
 
-// xg[s] = x[gather[s]], rows of K8 16-byte words: the operand that wgrad contracts over
-__global__ __launch_bounds__(256) void k_gather_rows(const uint4* __restrict__ x, const int32_t* __restrict__ gather,
-                                                     int64_t M, int64_t K8, uint4* __restrict__ xg)
-{
-    for (int64_t s = blockIdx.x; s < M; s += gridDim.x) {
-        const uint4* const from = x + (int64_t)gather[s] * K8;
-        for (int64_t k = threadIdx.x; k < K8; k += 256) xg[s * K8 + k] = from[k];
-    }
-}
-
-// da (or with h13: dh13 [M x 2K], and a [M x K] where it is not null) and dw, each where not null; xg:
-// rows in slot order for wgrad where gather is given
+// da (or with h13: dh13 [M x 2K], and a [M x K] where it is not null) and dw, each where not null
 hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
                                  const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
-                                 void* da, bool da_f32, uint16_t* act, uint16_t* xg, void* dw, bool dw_f32,
+                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32,
                                  hipStream_t stream)
 {
     if (da && M > 0) {
@@ -342,19 +332,15 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
         else group_gemm<false, FFN_BF16, false>(a, M, stream);
     }
     if (dw) {
-        if (gather && M > 0) {
-            const int64_t K8 = K / 8;
-            hipLaunchKernelGGL(k_gather_rows, dim3((unsigned)(M < 16384 ? M : 16384)), dim3(256), 0, stream,
-                               reinterpret_cast<const uint4*>(x), gather, M, K8, reinterpret_cast<uint4*>(xg));
-            x = xg;
-        }
         GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, dw, nullptr, nullptr, 0}, offsets, G, 0, 0, dw_f32 ? 4 : 2, 0};
+        a.p.gather = gather;
         auto run = [&](auto tile, auto epi) {
             typedef decltype(tile) T;
             a.p.rtiles = (K + T::BR - 1) / T::BR;
             a.p.ctiles = (N + T::BC - 1) / T::BC;
-            hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value>), dim3((unsigned)wgrad_grid(G, N, K, T::BR)), dim3(T::THREADS),
-                               0, stream, a);
+            const dim3 grid((unsigned)wgrad_grid(G, N, K, T::BR)), block(T::THREADS);
+            if (gather) hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, false>), grid, block, 0, stream, a);
         };
         typedef std::integral_constant<int, FFN_F32> F32;
         typedef std::integral_constant<int, FFN_BF16> BF16;

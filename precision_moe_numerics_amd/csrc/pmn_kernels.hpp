@@ -169,11 +169,10 @@ bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd);
 hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const uint16_t* w, const int64_t* offsets,
                                  int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out, uint16_t* h13,
                                  hipStream_t stream);
-// da (with h13: dh13 [M x 2K], and a [M x K] into act where it is not null) and dw, each where not null; xg
-// [M x K]: where wgrad's rows go in slot order (gather given)
+// da (with h13: dh13 [M x 2K], and a [M x K] into act where it is not null) and dw, each where not null
 hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
                                  const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
-                                 void* da, bool da_f32, uint16_t* act, uint16_t* xg, void* dw, bool dw_f32,
+                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32,
                                  hipStream_t stream);
 
 int gemv_most_pairs();

@@ -253,7 +253,7 @@ def test_streams_and_replayed_graph(P):
 
 
 def test_two_calls_at_once(P):
-    """Calls on two streams share nothing (each brings its workspace)."""
+    """Calls on two streams share nothing."""
     cs = [case([200, 31, 150], 264, 520, s, tokens=90) for s in (21, 22)]
     run = lambda c: P.moe_grouped_gemm_bwd_bf16(c["dy"], c["x"], c["w"], c["off"], c["M"], 264, gather=c["gather"])  # noqa: E731
     want = [run(c) for c in cs]
