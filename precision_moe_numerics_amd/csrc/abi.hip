@@ -654,7 +654,8 @@ int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const 
     if (epilogue != PMN_EPI_F32 && epilogue != PMN_EPI_BF16 && epilogue != PMN_EPI_SWIGLU) return PMN_EINVAL;
     if ((gates && epilogue == PMN_EPI_SWIGLU) || (add && !gates)) return PMN_EINVAL;
     if (bad_gemv_shape(T, k, G, N, K) || w_rows_per_outer < 32 || w_rows_per_outer % 32 != 0) return PMN_ESHAPE;
-    if (epilogue == PMN_EPI_SWIGLU && N % 64 != 0) return PMN_ESHAPE;
+    // SWIGLU: w3's rows lie up to 2^32 bytes of codes behind w1's
+    if (epilogue == PMN_EPI_SWIGLU && (N % 64 != 0 || N * K > ((int64_t)1 << 33))) return PMN_ESHAPE;
     if (!ids && (G != 1 || k != 1)) return PMN_EINVAL;
     // workgroups of 512 threads, one for 8 or 16 rows: a launch has fewer than 2^32 threads
     const int64_t experts = ids ? (T * k < G ? T * k : G) : 1;

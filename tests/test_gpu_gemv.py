@@ -206,6 +206,38 @@ def test_streams_and_replayed_graph(P):
         assert all(torch.equal(a, b) for a, b in zip(want, held)), r
 
 
+def test_as_many_pairs_as_there_may_be(P):
+    """4096 pairs of a contraction as long as LDS holds, in three tiles a workgroup."""
+    T, k, G, N, K = 512, 8, 48, 2048, 8192
+    wq, x, ids = weights(P, G, N, K, 25), mk((T, K), 1.0, 26), choose(T, k, G, 27)
+    y, e = ref_pairs(x, values(wq), ids, N, G)
+    within(P.moe_gemv_nvfp4(x, wq, N, ids, P.EPI_F32), y, e, "y")
+    h1, h3 = y.chunk(2, 2)
+    e1, e3 = e.chunk(2, 2)
+    a = h1 * torch.sigmoid(h1) * h3
+    within(P.moe_gemv_nvfp4(x, wq, N, ids, P.EPI_SWIGLU), a,
+           1.02 * (16 * U * (1 + h1.abs()) * a.abs() + 1.1 * (e1 * h3.abs() + e3 * h1.abs())), "swiglu")
+
+
+def test_two_calls_at_once(P):
+    """Calls with gates on two streams share nothing (each brings its workspace)."""
+    G, N, K, k = 8, 256, 1056, 3
+    wq = weights(P, G, N, K, 29)
+    cs = [(mk((T, K), 1.0, T), choose(T, k, G, T), torch.rand((T, k), generator=torch.Generator().manual_seed(T)).to(DEV))
+          for T in (5, 24)]
+    run = lambda c: P.moe_gemv_nvfp4(c[0], wq, N, c[1], gates=c[2])  # noqa: E731
+    want = [run(c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        got = []
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                got.append(run(c))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_weights_past_32_bits(P):
     """Codes past 2^32 bytes: 100 experts of 4096 x 22016 (4.5 GB)."""
     G, N, K = 100, 4096, 22016

@@ -67,7 +67,7 @@ def test_gemv_refusals(lib):
     assert f(T=-1) == ESHAPE and f(k=0) == ESHAPE and f(G=0) == ESHAPE and f(N=48) == ESHAPE and f(K=48) == ESHAPE
     assert f(N=96, epi=2) == ESHAPE and f(rpo=16) == ESHAPE and f(rpo=0) == ESHAPE and f(rpo=40) == ESHAPE
     assert f(T=4097, k=1) == ESHAPE and f(T=2049, k=2) == ESHAPE and f(T=1 << 40) == ESHAPE and f(N=0) == ESHAPE
-    assert f(T=4096, k=1, G=4096, N=1 << 20) == ESHAPE
+    assert f(T=4096, k=1, G=4096, N=1 << 20) == ESHAPE and f(epi=2, N=1 << 17, K=(1 << 16) + 32) == ESHAPE
     for q in ("x", "c", "s", "o", "out"):
         assert f(**{q: None}) == EINVAL, q
     assert f(T=20, gates=FAKE) == EWS and f(T=20, gates=FAKE, ws=FAKE, nb=size(20, 2, 64, 1) - 1) == EWS
