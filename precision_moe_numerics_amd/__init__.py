@@ -812,7 +812,8 @@ def _group_args(w: torch.Tensor, offsets: torch.Tensor, M: int, N: int, gather, 
     _need(offsets is not None and offsets.dtype == torch.int64 and offsets.dim() == 1 and offsets.numel() >= 2,
           "offsets must be int64 [G+1]")
     G = offsets.numel() - 1
-    _need(w.dtype == torch.bfloat16 and w.dim() == 2 and w.shape[0] == G * N, f"w must be bf16 [G*N, K] with {G * N} rows")
+    if w.dtype != torch.bfloat16 or w.dim() != 2 or w.shape[0] != G * N:
+        raise PmnError(f"w must be bf16 [G*N, K] with {G * N} rows")
     _index(gather, M, torch.int32, "gather")
     _debug_indices(what, offsets, M, gather, src_rows)
     return G, w.shape[1]
@@ -826,7 +827,8 @@ def moe_grouped_gemm_fwd_bf16(x: torch.Tensor, w: torch.Tensor, offsets: torch.T
     _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [rows, K]")
     _need(epilogue in (EPI_F32, EPI_BF16, EPI_SWIGLU), "epilogue must be EPI_F32, EPI_BF16 or EPI_SWIGLU")
     G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_fwd_bf16", x.shape[0])
-    _need(x.shape[1] == K, f"x must have {K} columns")
+    if x.shape[1] != K:
+        raise PmnError(f"x must have {K} columns")
     at = _device_of(w, "w")
     dev = w.device
     swiglu = epilogue == EPI_SWIGLU
@@ -859,13 +861,15 @@ def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: to
     _tensor(dy, (M, N), torch.bfloat16, "dy")
     dgrad, wgrad = bool(flags & BWD_DGRAD), bool(flags & BWD_WGRAD)
     for name, dt in (("da_dtype", da_dtype), ("db_dtype", db_dtype)):
-        _need(dt in (torch.bfloat16, torch.float32), f"{name} must be bf16 or fp32")
+        if dt not in (torch.bfloat16, torch.float32):
+            raise PmnError(f"{name} must be bf16 or fp32")
     _need(dgrad or da is None, "da needs BWD_DGRAD")
     _need(wgrad or db is None, "db needs BWD_WGRAD")
     _need(x is not None or not wgrad or h13 is not None, "the weight gradient needs x or h13")
     G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_bwd_bf16", 0 if x is None else x.shape[0])
     if x is not None:
-        _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == K, f"x must be bf16 [rows, {K}]")
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
+            raise PmnError(f"x must be bf16 [rows, {K}]")
     if h13 is not None:
         _tensor(h13, (M, 2 * K), torch.bfloat16, "h13")
         _need(gather is None and dgrad and da_dtype == torch.bfloat16, "h13 goes with BWD_DGRAD, a bf16 da and no gather")
@@ -907,15 +911,21 @@ def moe_gemv_nvfp4(x: torch.Tensor, wq: NVFP4, N: int, ids: Optional[torch.Tenso
     _need(epilogue in (EPI_F32, EPI_BF16, EPI_SWIGLU), "epilogue must be EPI_F32, EPI_BF16 or EPI_SWIGLU")
     _nvfp4(wq, "wq")
     T, K = x.shape[0], x.shape[-1]
-    _need(wq.cols == K, f"wq must have {K} columns")
-    _need(N > 0 and wq.rows % N == 0 and wq.rows > 0, f"wq must have a multiple of {N} rows")
-    G, k = wq.rows // N, 1
+    if wq.cols != K:
+        raise PmnError(f"wq must have {K} columns")
+    R = wq.rows
+    if N <= 0 or R % N != 0 or R == 0:
+        raise PmnError(f"wq must have a multiple of {N} rows")
+    G, k = R // N, 1
     if ids is not None:
-        _need(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == T, f"ids must be int32 [{T}, k]")
+        if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T:
+            raise PmnError(f"ids must be int32 [{T}, k]")
         k = ids.shape[1]
     else:
-        _need(G == 1, f"without ids wq must have {N} rows")
-    _need(x.dim() == 2 or x.shape[1] == k, f"x must have {k} rows a token")
+        if G != 1:
+            raise PmnError(f"without ids wq must have {N} rows")
+    if x.dim() == 3 and x.shape[1] != k:
+        raise PmnError(f"x must have {k} rows a token")
     if gates is not None:
         _tensor(gates, (T, k), torch.float32, "gates")
         _need(epilogue != EPI_SWIGLU, "gates do not go with EPI_SWIGLU")
