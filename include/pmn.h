@@ -485,7 +485,8 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
  * gates NULL: epilogue PMN_EPI_F32 or _BF16, out [T*k x N]; PMN_EPI_SWIGLU (N = 2F, rows 0..F-1 of each
  *   expert w1, F..2F-1 w3), out bf16 [T*k x F] = silu(h1) h3.
  * gates fp32 [T x k]: out [T x N] = sum_j gates[t, j] y[t, j] + add[t] (add NULL, or bf16 [T x N]: the shared
- *   expert's row), of fp32 (PMN_EPI_F32) or bf16; a pair whose id is outside [0, G) adds nothing.
+ *   expert's row), of fp32 (PMN_EPI_F32) or bf16; a pair whose id is outside [0, G) adds nothing, whatever
+ *   its gate is.
  * PMN_EINVAL: gates with SWIGLU, add without gates. N % 32 == 0 (SWIGLU: N % 64 == 0, N K <= 2^33), K % 32 == 0, N
  * and K <= 2^20, w_rows_per_outer % 32 == 0 (SWIGLU: F % w_rows_per_outer == 0 keeps w1 and w3 apart), T * k <= 4096
  * (PMN_ESHAPE). x, w_codes, w_scales, add and out 16-byte aligned. Workspace (with gates; 16-byte aligned, at

@@ -654,7 +654,7 @@ int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const 
     if (epilogue != PMN_EPI_F32 && epilogue != PMN_EPI_BF16 && epilogue != PMN_EPI_SWIGLU) return PMN_EINVAL;
     if ((gates && epilogue == PMN_EPI_SWIGLU) || (add && !gates)) return PMN_EINVAL;
     if (bad_gemv_shape(T, k, G, N, K) || w_rows_per_outer < 32 || w_rows_per_outer % 32 != 0) return PMN_ESHAPE;
-    // SWIGLU: w3's rows lie up to 2^32 bytes of codes behind w1's
+    // SWIGLU: w3's codes lie N K / 4 bytes behind w1's, in the same 32-bit offset as the row and k
     if (epilogue == PMN_EPI_SWIGLU && (N % 64 != 0 || N * K > ((int64_t)1 << 33))) return PMN_ESHAPE;
     if (!ids && (G != 1 || k != 1)) return PMN_EINVAL;
     // workgroups of 512 threads, one for 8 or 16 rows: a launch has fewer than 2^32 threads
@@ -675,7 +675,7 @@ int moe_gemv_nvfp4(const void* x, int x_per_pair, const uint8_t* w_codes, const 
     const hipError_t e = pmn::launch_gemv_pairs(xs, x_per_pair != 0, w_codes, w_scales, w_outer, w_rows_per_outer, ids,
                                                 (int)T, k, G, N, K, PMN_EPI_F32, workspace, hs(stream));
     if (e != hipSuccess) return PMN_ELAUNCH;
-    return status(pmn::launch_combine_rows(workspace, true, T * k, N, nullptr, gates, as, T, k, out,
+    return status(pmn::launch_combine_rows(workspace, true, T * k, N, nullptr, gates, ids, G, as, T, k, out,
                                            epilogue == PMN_EPI_F32, hs(stream)));
 }
 
@@ -693,7 +693,7 @@ int moe_combine_rows_fwd(const void* y, int y_dtype, int64_t M, int64_t H, const
     if (T == 0 || H == 0) return PMN_OK;
     if (!out || (M > 0 && !y)) return PMN_EINVAL;
     if (!aligned(y, 16) || !aligned(add, 16) || !aligned(out, 16) || !aligned(slot_of, 4) || !aligned(gates, 4)) return PMN_EALIGN;
-    return status(pmn::launch_combine_rows(y, y_dtype == PMN_DTYPE_F32, M, H, slot_of, gates,
+    return status(pmn::launch_combine_rows(y, y_dtype == PMN_DTYPE_F32, M, H, slot_of, gates, nullptr, 0,
                                            static_cast<const uint16_t*>(add), T, k, out, out_dtype == PMN_DTYPE_F32,
                                            hs(stream)));
 }

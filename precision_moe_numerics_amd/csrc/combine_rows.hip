@@ -80,8 +80,8 @@ PMN_DEV int64_t slot_at(const int32_t* slot_of, int64_t q, int64_t M)
 template <bool YF32, bool OF32>
 __global__ __launch_bounds__(256) void k_combine_rows(const void* __restrict__ y, int64_t M, int64_t H,
                                                       const int32_t* __restrict__ slot_of,
-                                                      const float* __restrict__ gates, const uint16_t* add,
-                                                      int64_t T, int k, int chunks, void* out)
+                                                      const float* __restrict__ gates, const int32_t* __restrict__ ids, int G,
+                                                      const uint16_t* add, int64_t T, int k, int chunks, void* out)
 {
     using namespace rows;
     const int64_t t = blockIdx.x / (unsigned)chunks;
@@ -96,8 +96,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(const void* __restrict__ y
         bool on[KB];
 #pragma unroll
         for (int j = 0; j < KB; j++) {
-            const int64_t s = j0 + j < k ? slot_at(slot_of, t * k + j0 + j, M) : -1;
-            on[j] = s >= 0;
+            const int64_t q = t * k + j0 + j, s = j0 + j < k ? slot_at(slot_of, q, M) : -1;
+            on[j] = s >= 0 && (!ids || (uint32_t)ids[q] < (uint32_t)G);
             gt[j] = on[j] && gates ? gates[t * k + j0 + j] : 1.0f;
             if (on[j]) w[j] = load8<YF32>(y, s * H + h);
         }
@@ -189,8 +189,8 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const void* __restrict
 static int row_threads(int64_t H) { return H >= 1024 ? 256 : H >= 512 ? 128 : 64; }
 
 hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, const int32_t* slot_of,
-                               const float* gates, const uint16_t* add, int64_t T, int k, void* out, bool out_f32,
-                               hipStream_t stream)
+                               const float* gates, const int32_t* ids, int G, const uint16_t* add, int64_t T, int k,
+                               void* out, bool out_f32, hipStream_t stream)
 {
     const int th = row_threads(H), chunks = (int)((H / 8 + th - 1) / th);
     // a launch has fewer than 2^32 threads
@@ -200,11 +200,12 @@ hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, 
         const dim3 grid((unsigned)(n * chunks)), block(th);
         const int32_t* so = slot_of ? slot_of + t0 * k : nullptr;
         const float* gt = gates ? gates + t0 * k : nullptr;
+        const int32_t* id = ids ? ids + t0 * k : nullptr;
         const uint16_t* ad = add ? add + t0 * H : nullptr;
         const uint8_t* yy = static_cast<const uint8_t*>(y) + (slot_of ? 0 : t0 * k * H * (y_f32 ? 4 : 2));
         const int64_t m = slot_of ? M : M - t0 * k;
         uint8_t* o = static_cast<uint8_t*>(out) + t0 * H * (out_f32 ? 4 : 2);
-#define PMN_ROWS(A, B) hipLaunchKernelGGL((k_combine_rows<A, B>), grid, block, 0, stream, yy, m, H, so, gt, ad, n, k, chunks, o)
+#define PMN_ROWS(A, B) hipLaunchKernelGGL((k_combine_rows<A, B>), grid, block, 0, stream, yy, m, H, so, gt, id, G, ad, n, k, chunks, o)
         if (y_f32) {
             if (out_f32) PMN_ROWS(true, true);
             else PMN_ROWS(true, false);

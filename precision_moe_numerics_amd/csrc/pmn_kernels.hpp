@@ -181,10 +181,10 @@ int gemv_most_pairs();
 hipError_t launch_gemv_pairs(const uint16_t* x, bool per_pair, const uint8_t* codes, const uint8_t* scales,
                              const float* outer, int64_t rpo, const int32_t* ids, int T, int k, int G, int64_t N,
                              int64_t K, int epilogue, void* out, hipStream_t stream);
-// slot_of null: pair q is slot q; gates null: ones
+// slot_of null: pair q is slot q; gates null: ones; ids not null: pairs whose id is outside [0, G) add nothing
 hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, const int32_t* slot_of,
-                               const float* gates, const uint16_t* add, int64_t T, int k, void* out, bool out_f32,
-                               hipStream_t stream);
+                               const float* gates, const int32_t* ids, int G, const uint16_t* add, int64_t T, int k,
+                               void* out, bool out_f32, hipStream_t stream);
 hipError_t launch_combine_rows_bwd(const void* dout, bool d_f32, const void* y, bool y_f32, int64_t M, int64_t H,
                                    const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy,
                                    float* dgates, hipStream_t stream);

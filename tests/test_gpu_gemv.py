@@ -129,6 +129,18 @@ def test_repeated_and_outside_ids(P, T):
     check(P, T, k, G, 64, 352, none, True, 300 + T)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_an_outside_pairs_gate_is_not_read(P, value):
+    G, k, N, K = 5, 4, 64, 352
+    wq, x = weights(P, G, N, K, 31), mk((6, K), 1.0, 32)
+    ids = choose(6, k, G, 33)
+    ids[0, 1], ids[3], ids[5, 3] = -1, G, 1 << 30
+    gates = torch.rand((6, k), generator=torch.Generator().manual_seed(34)).to(DEV)
+    bad = torch.where((ids < 0) | (ids >= G), torch.full_like(gates, value), gates)
+    a, b = (P.moe_gemv_nvfp4(x, wq, N, ids, P.EPI_F32, gates=g) for g in (gates, bad))
+    assert torch.isfinite(b).all() and torch.equal(a, b) and (b[3] == 0).all()
+
+
 def test_tokens_keep_to_themselves(P):
     """A token's NaN or infinity reaches its own rows only, and an expert's NaN scale the tokens that name it."""
     T, k, G, N, K = 9, 3, 6, 64, 256
