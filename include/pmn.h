@@ -517,7 +517,7 @@ int moe_combine_rows_fwd(const void* y, int y_dtype, int64_t M, int64_t H, const
  *   dgates[t, j] = sum_h dout[t, h] y[slot_of[t, j], h]   fp32 [T x k], or NULL (then y may be NULL)
  * Rows of dy that no pair names are left as they are; a pair whose slot is outside [0, M) writes no row and
  * its dgates is zero. No slot may be named twice: its row of dy would be one pair's, not their sum. Sizes and
- * alignment as the forward; dy and dgates not both NULL (PMN_EINVAL).
+ * alignment as the forward; dy and dgates not both NULL where T and M are positive (PMN_EINVAL).
  */
 int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype, int64_t M, int64_t H,
                          const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy, float* dgates,

@@ -1003,6 +1003,7 @@ def moe_combine_rows_bwd(dout: torch.Tensor, y: torch.Tensor, slot_of: torch.Ten
     if CHECK_INDICES and want_dy:
         inside = slot_of[(slot_of >= 0) & (slot_of < M)]
         _need(inside.unique().numel() == inside.numel(), "moe_combine_rows_bwd: a slot is named twice")
+        _need(dy is not None or M != T * k or inside.numel() == M, "moe_combine_rows_bwd: a row of the new dy is no pair's")
     if want_dy and dy is None:
         dy = torch.empty_like(y) if M == T * k else torch.zeros_like(y)
     dgates = torch.empty((T, k), dtype=torch.float32, device=y.device) if want_dgates else None

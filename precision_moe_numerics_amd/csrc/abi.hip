@@ -704,8 +704,8 @@ int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_
 {
     if (bad_dtype(dout_dtype) || bad_dtype(y_dtype)) return PMN_EINVAL;
     if (bad_rows_shape(M, H, T, k) || (!slot_of && M < T * k)) return PMN_ESHAPE;
-    if (!dy && !dgates) return PMN_EINVAL;
     if (T == 0) return PMN_OK;
+    if (!dy && !dgates) return M > 0 ? PMN_EINVAL : PMN_OK;   // dy without rows may have no address
     if (H > 0 && (!dout || (dgates && M > 0 && !y))) return PMN_EINVAL;
     if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(dgates, 4) || !aligned(slot_of, 4) ||
         !aligned(gates, 4))

@@ -132,6 +132,32 @@ def test_nothing_to_do(P):
     assert dy.shape == (0, 64) and (dg == 0).all()
 
 
+def test_backward_of_no_rows(P):
+    empty = torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV)
+    dy, dg = P.moe_combine_rows_bwd(empty, empty, torch.zeros((0, 3), dtype=torch.int32, device=DEV))
+    assert dy.shape == (0, 64) and dg.shape == (0, 3)
+    out = torch.ones((2, 64), dtype=torch.bfloat16, device=DEV)
+    dy, dg = P.moe_combine_rows_bwd(out, empty, torch.zeros((2, 3), dtype=torch.int32, device=DEV), want_dgates=False)
+    assert dy.shape == (0, 64) and dg is None
+
+
+def test_checked_indices(P, monkeypatch):
+    """With CHECK_INDICES a slot named twice, and a new dy with rows that no pair writes, are refused."""
+    monkeypatch.setattr(P, "CHECK_INDICES", True)
+    y, dout = mk((6, 64), 1.0, 1, torch.float32), mk((2, 64), 1.0, 2, torch.float32)
+    so = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32, device=DEV)
+    P.moe_combine_rows_bwd(dout, y, so)
+    so[1, 2] = -1
+    with pytest.raises(P.PmnError):
+        P.moe_combine_rows_bwd(dout, y, so)
+    dy = torch.zeros_like(y)
+    P.moe_combine_rows_bwd(dout, y, so, dy=dy)
+    assert (dy[5] == 0).all()
+    so[1, 2] = 0
+    with pytest.raises(P.PmnError):
+        P.moe_combine_rows_bwd(dout, y, so, dy=dy)
+
+
 def test_a_slots_nan_stays_with_its_token(P):
     y, so = mk((40, 136), 1.0, 1, torch.bfloat16), slots(10, 4, 40, 2)
     gates = mk((10, 4), 1.0, 3, torch.float32)

@@ -301,6 +301,22 @@ def test_offsets_past_32_bits(P):
         within(y[s], want, (K + 2) * U * (x[s].double().abs() @ w[g * N:(g + 1) * N].double().abs().t()), f"row {s}")
 
 
+def test_gathered_weight_gradient_through_large_tiles_past_32_bits(P):
+    """x rows past 2^32 bytes as gathered k of 256 x 256 tiles, groups without and with one slot between."""
+    N, K, rows = 1040, 4104, 600000             # 4.9 GB of rows
+    counts = [700, 0, 1, 3000, 1500, 900, 2000, 255]
+    M = sum(counts)
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(51)
+    at = torch.cat([torch.randint(0, rows, (997,), generator=g), torch.tensor([0, rows - 1, rows - 2])]).to(DEV)
+    x[at] = mk((1000, K), 1.0, 52)
+    gather = at[torch.randint(0, 1000, (M,), generator=g).to(DEV)].to(torch.int32)
+    dy, w, off = mk((M, N), 1.0, 53), mk((8 * N, K), 0.02, 54), offsets_of(counts)
+    _, dw = P.moe_grouped_gemm_bwd_bf16(dy, x, w, off, M, N, flags=P.BWD_WGRAD, gather=gather)
+    _, dw2 = P.moe_grouped_gemm_bwd_bf16(dy, x[gather.long()], w, off, M, N, flags=P.BWD_WGRAD)
+    assert torch.equal(dw, dw2) and dw.view(8, -1).abs().amax(1).gt(0).tolist() == [c > 0 for c in counts]
+
+
 def test_gradients_agree_with_differences(P):
     """<dw, v> and <da, v> against central differences of the fp64 loss sum(y dy): the loss is bilinear, so a central
     difference is exact up to rounding; bounds as above, summed with |v|."""

@@ -96,6 +96,13 @@ def test_combine_refusals(lib):
     assert f(T=0, y=None, out=None) == 0 and b(T=0, d=None, y=None) == 0
 
 
+def test_combine_backward_of_nothing(lib):
+    """Tensors without values have no address: no tokens, or no rows and no dgates, is no error."""
+    f = lambda T, M, dy, dg: lib.moe_combine_rows_bwd(FAKE, 0, FAKE, 0, M, 64, FAKE, FAKE, T, 2, dy, dg, None)  # noqa: E731
+    assert f(0, 0, None, None) == 0 and f(0, 8, FAKE, None) == 0 and f(4, 0, None, None) == 0
+    assert f(4, 8, None, None) == EINVAL
+
+
 def bf(*shape):
     return torch.zeros(shape, dtype=torch.bfloat16)
 
