@@ -14,7 +14,9 @@
 // descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
 // the same code.
 //   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
-//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured).
+//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured). Where both operands are KC,
+//     two stages at a time: rows of 128 bytes, chunk c at slot c ^ ((r / 2) % 8), so that a load takes whole
+//     lines of 8 rows and not halves of 16 (49152 x 4096 x 7168: 2130 us with halves, 2025 so).
 //   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
 //     of 16 the column i of 4 k; the 32-byte pairs of chunks of row k are permuted by
 //     ((k / 8) % 2) | 2 (k % 4), so that the 4 k of 16 lanes lie in different banks (174 B/clk/CU
@@ -146,7 +148,8 @@ PMN_DEV void dma16_flat(const void* src, uint32_t lds)
 }
 static __device__ const uint4 ffn_zeros = {0u, 0u, 0u, 0u};   // what a gathered chunk outside the operand reads
 
-// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of 5 filled in pairs
+// WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of two and a half or three pairs
+// of them (PAIRS, where both operands are k-contiguous)
 template <int WR_, int WC_, int RB_, int CB_, int NST_>
 struct FfnTile {
     static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
@@ -159,10 +162,10 @@ struct FfnTile {
     static constexpr bool HALVES = RB_ * CB_ == 16;
     typedef FfnTile<WR_, WC_, RB_, CB_ / 2, NST_> Half;         // of the output rows, all of the columns
     static constexpr bool PAIRS = RPW % 2 == 0 && CPW % 2 == 0;
-    static constexpr int RING = (PAIRS ? 5 : NST) * STAGE, OUTB = OROWS * OPITCH * 4;
+    static constexpr int RING = !PAIRS ? NST * STAGE : BR == BC ? 5 * BR * 128 : 3 * (BR + BC) * 128, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
-    static_assert((PAIRS ? 6 : NST - 1) * (PPW + 1) <= 63, "vmcnt");
+    static_assert((PAIRS ? 6 : NST - 1) * (PPW + 1) <= 63, "vmcnt");   // loads on their way before the first wait
 };
 
 // Item number of workgroup L among n: workgroups L, L + 8, .. run on one XCD and take consecutive items.
@@ -195,8 +198,10 @@ template <typename T, bool RKC, bool CKC, int EPI, int GATHER = GATHER_NONE>
 PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, uint8_t* lds)
 {
     constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, PPW = T::PPW;
-    constexpr bool SWI = EPI == FFN_SWIGLU, PAIRED = T::PAIRS && RKC && CKC;
-    constexpr int NST = PAIRED ? 5 : T::NST;
+    constexpr bool SWI = EPI == FFN_SWIGLU, LINES = T::PAIRS && RKC && CKC;
+    constexpr int NST = T::NST;
+    constexpr int NR = LINES ? 2 * T::RPW : T::RPW, NC = LINES ? 2 * T::CPW : T::CPW, NPC = NR + NC;   // pieces of a wavefront
+    constexpr int PROWS = LINES ? 8 : 16;   // rows of a k-contiguous operand's piece
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
     static_assert(GATHER != GATHER_C || CKC, "C's rows are gathered where it is k-contiguous");
     static_assert(GATHER != GATHER_R || (!RKC && !CKC && EPI != FFN_PART), "R's k are gathered where it is row-contiguous, in wgrad");
@@ -219,21 +224,21 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     // the same lines at once: 4 to 5% at 128 x 128 (600 .. 2000 rows forward); 256 x 256 tiles are bound by
     // their MFMAs and run 1% slower with it.
     constexpr bool ROTATE = RB * CB < 16;
-    const int rotr = ROTATE ? (int)(tcol % (BR / 16)) : 0, rotc = ROTATE ? (int)(trow % (BC / 16)) : 0;
+    const int rotr = ROTATE ? (int)(tcol % (BR / PROWS)) : 0, rotc = ROTATE ? (int)(trow % (BC / PROWS)) : 0;
     auto piece_of = [&](int i) {   // piece of its operand's tile
-        return i < T::RPW ? (wave * T::RPW + i + rotr) % (BR / 16) : (wave * T::CPW + i - T::RPW + rotc) % (BC / 16);
+        return i < NR ? (wave * NR + i + rotr) % (BR / PROWS) : (wave * NC + i - NR + rotc) % (BC / PROWS);
     };
-    uint32_t voff[PPW];
-    int kch[PPW];
-    const uint8_t* from[GATHER == GATHER_C ? T::CPW : 1];   // the gathered rows' chunks at this part's first stage
+    uint32_t voff[NPC];
+    int kch[NPC];
+    const uint8_t* from[GATHER == GATHER_C ? NC : 1];   // the gathered rows' chunks at this part's first stage
 #pragma unroll
-    for (int i = 0; i < PPW; i++) {
-        const bool isr = i < T::RPW;
+    for (int i = 0; i < NPC; i++) {
+        const bool isr = i < NR;
         const int q = piece_of(i);
         const int64_t ld = isr ? p.ldr : p.ldc;
         if (isr ? RKC : CKC) {
-            const int t = q * 16 + (lane >> 2);                       // tile row
-            const int ch = (lane & 3) ^ ((t >> 2) & 3);
+            const int t = LINES ? q * 8 + (lane >> 3) : q * 16 + (lane >> 2);   // tile row
+            const int ch = LINES ? (lane & 7) ^ ((t >> 1) & 7) : (lane & 3) ^ ((t >> 2) & 3);
             int row = t;                                              // from the tile's first
             bool ok;
             if (SWI && isr) {
@@ -246,7 +251,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             voff[i] = ok ? (uint32_t)(row * ld * 2 + ch * 16) : FFN_OUTSIDE;
             kch[i] = ch * 8;
             if (GATHER == GATHER_C && !isr) {
-                from[i - T::RPW] = ok ? reinterpret_cast<const uint8_t*>(p.c + (int64_t)p.gather[c0 + t] * ld + s0 * 32 + ch * 8)
+                from[i - NR] = ok ? reinterpret_cast<const uint8_t*>(p.c + (int64_t)p.gather[c0 + t] * ld + s0 * 32 + ch * 8)
                                       : nullptr;
                 if (!ok) kch[i] = 0x7FFFFFFF;   // past every stage
             }
@@ -277,11 +282,11 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         int rrec, crec;   // and bytes from there
         uint32_t at;
         int left;         // k from the stage's first to the part's end: none where it is not positive
-        uint32_t dst;
+        uint32_t dst, dstc;   // where R's and C's pieces go
     };
     const uint64_t r3 = SWI ? (uint64_t)p.F * p.ldr * 2 : 0;   // from w1's rows to w3's
     constexpr bool ONE_HALF = SWI && !ROTATE && RB % T::RPW == 0;   // a wavefront's pieces of R are all of w1 or all of w3
-    auto of_w3 = [&](int i) { return SWI && (piece_of(i) >> 1) % RB >= RB / 2; };
+    auto of_w3 = [&](int i) { return SWI && ((piece_of(i) * PROWS) >> 5) % RB >= RB / 2; };
     auto records = [&](int left, int64_t ld, int64_t at) {
         const int rows = left < 64 ? left : 64;
         return rows > 0 ? (int)((rows * (int)ld - (int)at) * 2) : 0;
@@ -296,6 +301,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         g.rrec = RKC ? 0x7FFFFFFF : records(g.left, p.ldr, r0);
         g.crec = CKC ? 0x7FFFFFFF : records(g.left, p.ldc, c0);
         g.dst = (uint32_t)(s % NST) * T::STAGE + lds0;
+        g.dstc = g.dst + T::RBYTES;
         return g;
     };
     // the same `by` stages on; in scalar instructions few enough for the gap between two MFMAs
@@ -305,6 +311,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         g.at += 64 * BY;
         g.dst += BY * T::STAGE;
         g.dst = g.dst >= lds0 + NST * T::STAGE ? g.dst - NST * T::STAGE : g.dst;
+        g.dstc = g.dst + T::RBYTES;
         if (!RKC && GATHER != GATHER_R) {
             g.r += (uint64_t)(64 * BY) * p.ldr;
             g.rrec = records(g.left, p.ldr, r0);
@@ -319,7 +326,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
                      __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
     };
     // Piece i's lane offset in stage g: chunks past the part's end of a k-contiguous operand lie outside
-    auto lane_offset = [&](const Stage& g, int i) { return (i < T::RPW ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i]; };
+    auto lane_offset = [&](const Stage& g, int i) { return (i < NR ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i]; };
     struct Index {
         uint32_t v[GATHER == GATHER_R ? T::RPW : 1];
     };
@@ -341,16 +348,16 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         return x;
     };
     auto issue_piece = [&](const Stage& g, int i, uint32_t v) {
-        const bool isr = i < T::RPW;
+        const bool isr = i < NR;
         if (GATHER == GATHER_R && isr) {
             const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
             const uint8_t* row = reinterpret_cast<const uint8_t*>(p.r + r0) + (uint64_t)index.v[i] * (uint64_t)(uint32_t)(p.ldr * 2) + voff[i];
             dma16_flat(kch[i] >= g.left ? z : row, g.dst + piece_of(i) * 1024);
         } else if (GATHER == GATHER_C && !isr) {
             const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
-            dma16_flat(kch[i] >= g.left ? z : from[i - T::RPW] + g.at, g.dst + T::RBYTES + piece_of(i) * 1024);
+            dma16_flat(kch[i] >= g.left ? z : from[i - NR] + g.at, g.dstc + piece_of(i) * 1024);
         } else if (!isr) {
-            dma16_buffer(descriptor(g.c, g.crec), v, CKC ? g.at : 0u, g.dst + T::RBYTES + piece_of(i) * 1024);
+            dma16_buffer(descriptor(g.c, g.crec), v, CKC ? g.at : 0u, g.dstc + piece_of(i) * 1024);
         } else {
             dma16_buffer(descriptor(!ONE_HALF && of_w3(i) ? g.r + r3 : g.r, g.rrec), v, RKC ? g.at : 0u, g.dst + piece_of(i) * 1024);
         }
@@ -360,10 +367,12 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         bf16x8 r[RB][2], c[CB][2];
     };
     // lane constants of the fragment reads
-    const int swz = (l32 >> 2) & 3;
+    const int swz = (l32 >> 2) & 3, swl = (l32 >> 1) & 7;
     const int g16 = lane >> 4, i16 = lane & 15, swt = (g16 >> 1) | ((i16 >> 2) << 1);
-    auto read_frag = [&](const uint8_t* base, auto kc, int width, int blk, int ks) -> bf16x8 {
-        if constexpr (decltype(kc)::value) {
+    auto read_frag = [&](const uint8_t* base, auto kc, int width, int blk, int ks, int half) -> bf16x8 {
+        if constexpr (decltype(kc)::value && LINES) {
+            return *reinterpret_cast<const bf16x8*>(base + (blk * 32 + l32) * 128 + (((4 * half + 2 * ks + hh) ^ swl) << 4));
+        } else if constexpr (decltype(kc)::value) {
             return *reinterpret_cast<const bf16x8*>(base + (blk * 32 + l32) * 64 + (((2 * ks + hh) ^ swz) << 4));
         } else {
             // columns 32 blk + 16 (g16 % 2) .., k = 16 ks + 8 (g16 / 2) + i16 / 4 and 4 further
@@ -375,10 +384,15 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         }
     };
     constexpr int NREAD = 2 * (RB + CB);   // fragments of a stage, in the order of their use
-    auto read_one = [&](const uint8_t* base, int n, Frags& f) {
+    struct Place {   // a stage's fragments
+        const uint8_t *r, *c;
+        int half;    // LINES: of its pair
+    };
+    auto place_of = [&](int s) { return Place{lds + (s % NST) * T::STAGE, lds + (s % NST) * T::STAGE + T::RBYTES, 0}; };
+    auto read_one = [&](const Place& at, int n, Frags& f) {
         const int ks = n / (RB + CB), b = n % (RB + CB);
-        if (b < RB) f.r[b][ks] = read_frag(base, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks);
-        else f.c[b - RB][ks] = read_frag(base + T::RBYTES, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks);
+        if (b < RB) f.r[b][ks] = read_frag(at.r, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks, at.half);
+        else f.c[b - RB][ks] = read_frag(at.c, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks, at.half);
     };
 
     f32x16 acc[RB][CB];
@@ -397,8 +411,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     constexpr int NM = 2 * RB * CB, NRQ = NM * 3 / 4;
     constexpr bool ROOMY = NM >= 2 * (NREAD / 2 + PPW);   // loads and reads have places of their own
     auto load_of = [](int q) { return (q + 1) * PPW / NM > q * PPW / NM ? q * PPW / NM : -1; };   // at most one a place where ROOMY
-    auto compute = [&](int next, const Frags& cur, Frags& nxt, auto ready, auto load, auto other) {
-        const uint8_t* rbase = lds + (next % NST) * T::STAGE;
+    auto compute = [&](const Place& next, const Frags& cur, Frags& nxt, auto ready, auto load, auto other) {
         int read = 0;
         uint32_t v[PPW];
 #pragma unroll
@@ -408,10 +421,10 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             if constexpr (ROOMY) {
                 if (q + 1 < NM && load_of(q + 1) >= 0) v[load_of(q + 1)] = ready(load_of(q + 1));
                 if (load_of(q) >= 0) load(load_of(q), v[load_of(q)]);
-                else if (read < NREAD) read_one(rbase, read++, nxt);
+                else if (read < NREAD) read_one(next, read++, nxt);
             } else {
 #pragma unroll
-                for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(rbase, n, nxt);
+                for (int n = q * NREAD / NRQ; n < (q + 1) * NREAD / NRQ && n < NREAD; n++) read_one(next, n, nxt);
 #pragma unroll
                 for (int n = q * PPW / NM; n < (q + 1) * PPW / NM; n++) load(n, ready(n));
             }
@@ -420,14 +433,13 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         }
     };
     Frags f0, f1;
-    auto read_first = [&] {
+    auto read_first = [&](const Place& at) {
 #pragma unroll
-        for (int n = 0; n < NREAD; n++) read_one(lds, n, f0);
+        for (int n = 0; n < NREAD; n++) read_one(at, n, f0);
     };
     const std::integral_constant<int, 1> one;
-    const std::integral_constant<int, 2> two;
     constexpr int LATE = NM * 3 / 4;   // where the next stages' scalars are formed
-    if constexpr (!PAIRED) {
+    if constexpr (!LINES) {
         Stage g = stage_at(0);
         if constexpr (GATHER == GATHER_R) {
             Index at[NST];
@@ -452,7 +464,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             }
         }
         wait_loads_and_barrier<(NST - 1) * LPS>();
-        read_first();
+        read_first(place_of(0));
         if constexpr (GATHER == GATHER_R) index = read_index(NST);
         // stage v + 1 has landed and every wavefront is done reading stage v, whose slot is refilled
         auto step = [&](int v, const Frags& cur, Frags& nxt) {
@@ -460,7 +472,7 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             const Stage h = g;   // stage v + NST
             Index ahead;
             if constexpr (GATHER == GATHER_R) ahead = read_index(v + NST + 1);
-            compute(v + 1, cur, nxt, [&](int n) { return lane_offset(h, n); }, [&](int n, uint32_t o) { issue_piece(h, n, o); },
+            compute(place_of(v + 1), cur, nxt, [&](int n) { return lane_offset(h, n); }, [&](int n, uint32_t o) { issue_piece(h, n, o); },
                     [&](int q) {
                         if (q == LATE) advance(g, one);
                         if constexpr (GATHER == GATHER_R)
@@ -474,46 +486,75 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         }
     } else {
         // Both operands k-contiguous: a row gives 64 bytes to a stage, half a 128-byte line. Stages go in
-        // pairs v, v + 1 (v even): a piece is loaded for both stages back to back, so that the second half
-        // of its lines is in the first-level cache (8192 x 7168 x 2048 forward: 707 us with single stages,
-        // 660 in pairs; row-contiguous operands, whose stages are whole lines, lose 5% by it). Slots of
-        // stages v - 1 and v are free at step v; half of the pieces are loaded then, half at step v + 1.
-        Stage g0 = stage_at(0), g1 = stage_at(1);
-#pragma unroll
-        for (int s = 0; s < NST - 1; s += 2) {
-#pragma unroll
-            for (int i = 0; i < PPW; i++) {
-                issue_piece(g0, i, lane_offset(g0, i));
-                issue_piece(g1, i, lane_offset(g1, i));
+        // pairs, and a piece is 8 rows of a pair, whole lines. Pair p's first stage is multiplied while the
+        // fragments of its second are read (its even step), its second while those of pair p + 1's first are
+        // (its odd step), so that its slots are free from its odd step on. LDS holds two and a half pairs of
+        // equal operands, as slots of one operand of a pair: R of pair p + 2 is loaded in the even step and C of
+        // it in the odd one; or three pairs: half of pair p + 2's pieces, then half of pair p + 3's. (8192 x 7168 x 2048
+        // forward: 707 us with single stages, 660 with pairs of half lines; halves to whole lines as above. A second
+        // barrier, before the even step, changes nothing. Row-contiguous operands, whose stages are whole lines,
+        // lose 5% by pairs.)
+        constexpr bool EQUAL = BR == BC;
+        constexpr uint32_t RPB = BR * 128, CPB = BC * 128, RING = EQUAL ? 5 * RPB : 3 * (RPB + CPB);
+        struct At {
+            uint32_t r, c;
+        };
+        auto next_pair = [](At& a) {
+            if (EQUAL) {
+                a.r = a.r >= 3 * RPB ? a.r - 3 * RPB : a.r + 2 * RPB;
+                a.c = a.c >= 3 * RPB ? a.c - 3 * RPB : a.c + 2 * RPB;
+            } else {
+                a.r = a.r + RPB + CPB == RING ? 0 : a.r + RPB + CPB;
+                a.c = a.r + RPB;
             }
-            advance(g0, two);
-            advance(g1, two);
+        };
+        At to{0, RPB}, in{0, RPB};
+        Stage g = stage_at(0);
+        g.dst = lds0 + to.r;
+        g.dstc = lds0 + to.c;
+        auto next_loads = [&] {
+            next_pair(to);
+            g.left -= 64;
+            g.at += 128;
+            g.dst = lds0 + to.r;
+            g.dstc = lds0 + to.c;
+        };
+        // piece n of those that a step loads
+        auto piece = [](int n, bool odd) {
+            if (EQUAL) return odd ? NR + n : n;
+            const int h = odd ? 0 : 1;
+            return n < NR / 2 ? h * (NR / 2) + n : NR + h * (NC / 2) + n - NR / 2;
+        };
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+#pragma unroll
+            for (int i = 0; i < NPC; i++) issue_piece(g, i, lane_offset(g, i));
+            next_loads();
         }
-        wait_loads_and_barrier<(NST - 3) * PPW>();
-        read_first();
-        auto step = [&](int v, auto second, const Frags& cur, Frags& nxt) {
-            constexpr int odd = decltype(second)::value ? 1 : 0;
-            auto piece = [&](int n) {
-                const bool isr = n < T::RPW;
-                const int m = isr ? n : n - T::RPW, half = (isr ? T::RPW : T::CPW) / 2;
-                return (isr ? 0 : T::RPW) + odd * half + (m >> 1);
-            };
-            auto stage = [&](int n) -> const Stage& { return ((n < T::RPW ? n : n - T::RPW) & 1) ? g1 : g0; };
-            compute(v + odd + 1, cur, nxt, [&](int n) { return lane_offset(stage(n), piece(n)); },
-                    [&](int n, uint32_t o) { issue_piece(stage(n), piece(n), o); }, [](int) {});
+        if (!EQUAL) {
+#pragma unroll
+            for (int i = 0; i < PPW; i++) issue_piece(g, piece(i, true), lane_offset(g, piece(i, true)));
+        }
+        wait_loads_and_barrier<EQUAL ? NPC : NPC + PPW>();
+        auto stage_in = [&](int half) { return Place{lds + in.r, lds + in.c, half}; };
+        read_first(stage_in(0));
+        auto step = [&](auto second, const Frags& cur, Frags& nxt) {
+            constexpr bool odd = decltype(second)::value;
+            compute(stage_in(odd ? 0 : 1), cur, nxt, [&](int n) { return lane_offset(g, piece(n, odd)); },
+                    [&](int n, uint32_t o) { issue_piece(g, piece(n, odd), o); }, [](int) {});
         };
         for (int v = 0; v < nst; v += 2) {
-            wait_loads_and_barrier<63>();      // stage v + 1 landed with its pair
-            step(v, std::false_type{}, f0, f1);
-            wait_loads_and_barrier<PPW>();     // the pair v + 2, v + 3: all but step v's loads
-            step(v, std::true_type{}, f1, f0);
-            advance(g0, two);
-            advance(g1, two);
+            step(std::false_type{}, f0, f1);
+            next_pair(in);
+            if (!EQUAL) next_loads();
+            wait_loads_and_barrier<EQUAL ? NR : NPC>();   // pair p + 1 has landed
+            step(std::true_type{}, f1, f0);
+            if (EQUAL) next_loads();
         }
     }
     wait_loads_and_barrier<0>();
 
-    // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]; a thread finishes NP pieces
+    // output rows c0 + wc * 32 CB + j * 32 .., staged as fp32 [WC * 32][BR]; a thread finishes NPC pieces
     // of 8 values, whose words of aux are on their way while the rows are staged
     float* const ot = reinterpret_cast<float*>(lds);
     constexpr int NW = (SWI ? BR / 2 : BR) / 8, NP = T::OROWS * NW / T::THREADS;

@@ -23,6 +23,7 @@ struct GroupArgs {
     int64_t out_width;        // output elements of a slot, and bytes of each
     int out_bytes;
     int64_t out2_width;
+    bool apart;               // half tiles run after the whole ones
 };
 
 // Moves p to group g, whose slots are s0 .. s1
@@ -39,12 +40,13 @@ PMN_DEV void group_at(const GroupArgs& a, int g, int64_t s0, int64_t s1, FfnArgs
     if (p.aux) p.aux += s0 * 2 * p.F;
 }
 
-// Units of `unit` slots over all groups, on the device.
-PMN_DEV int64_t group_units(const int64_t* offsets, int G, int64_t unit)
+// Units over all groups, count(slots) each, on the device.
+template <typename F>
+PMN_DEV int64_t group_units(const int64_t* offsets, int G, F count)
 {
     const int lane = threadIdx.x & 63;
     int64_t n = 0;
-    for (int g = lane; g < G; g += 64) n += (offsets[g + 1] - offsets[g] + unit - 1) / unit;
+    for (int g = lane; g < G; g += 64) n += count(offsets[g + 1] - offsets[g]);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, 64);
     return n;
@@ -58,19 +60,27 @@ PMN_DEV int64_t uniform64(int64_t v)
 
 // Workgroup L's tile of a product over the groups' slots: units of `unit` slots, a.p.rtiles tiles
 // of R each. Consecutive tiles of a group run on one XCD in bands of 8 tiles of R, so that they share
-// panels of both operands in its L2. False past the last.
+// panels of both operands in its L2. With a.apart the units of at most unit / 2 slots run after all others.
+// False past the last.
 template <bool GATHER>
 PMN_DEV bool group_tile(const GroupArgs& a, int64_t L, int64_t unit, FfnArgs& p, int64_t& trow, int64_t& tcol)
 {
-    const int64_t i = ffn_item_of(uniform64(group_units(a.offsets, a.G, unit)) * a.p.rtiles, L);
+    const int64_t least = a.apart ? unit / 2 : 0;   // slots that a unit of the first ones has more than
+    auto firsts = [=](int64_t n) { return (n + unit - 1 - least) / unit; };
+    auto others = [=](int64_t n) { return (n + unit - 1) / unit - (n + unit - 1 - least) / unit; };
+    const int64_t n = uniform64(group_units(a.offsets, a.G, firsts)) * a.p.rtiles, per = (n + 7) >> 3;
+    const bool late = (L >> 3) >= per;
+    if (late && !a.apart) return false;
+    const int64_t i = late ? ffn_item_of(uniform64(group_units(a.offsets, a.G, others)) * a.p.rtiles, L - per * 8) : ffn_item_of(n, L);
     if (i < 0) return false;
     const int64_t u = i / a.p.rtiles;
-    const GroupUnit w = locate_group_unit(a.offsets, a.G, u, unit);
+    const GroupUnit w = late ? locate_group(a.offsets, a.G, u, others) : locate_group(a.offsets, a.G, u, firsts);
     if (w.g < 0) return false;
     const int64_t s0 = uniform64(w.s0), s1 = uniform64(w.s1), first = u - uniform64(w.index);
     group_at<GATHER>(a, __builtin_amdgcn_readfirstlane(w.g), s0, s1, p);
-    p.ctiles = (s1 - s0 + unit - 1) / unit;
+    p.ctiles = late ? 1 : firsts(s1 - s0);
     ffn_tile_at(p, i - first * a.p.rtiles, trow, tcol);
+    if (late) tcol = firsts(s1 - s0);
     return true;
 }
 
@@ -204,20 +214,20 @@ typedef FfnTile<2, 2, 2, 1, 4> GroupSlim;    // 128 x 64
 
 // Tiles and their times of one round of 256 workgroups, in us of a contraction of 4096 plus what a tile
 // takes beside it (first loads, epilogue), taken from 60 sizes of 1 to 48 groups; half: a large tile of at most
-// 128 slots, as nearly all are where the groups' mean is that small.
+// 128 slots, as nearly all are where the groups' mean is that small; alone: where there is no second round
+// (two mid tiles fit a CU and slow each other).
 struct GroupTile {
     int br, bc;
-    double full, half, rest;
+    double full, half, alone, rest;
 };
 enum { GROUP_LARGE = 0, GROUP_MID = 1, GROUP_SLIM = 2, GROUP_FEW = 3 };
-static const GroupTile GROUP_TILES[4] = {{256, 256, 80.0, 49.0, 14.0}, {128, 128, 36.0, 36.0, 2.0},
-                                         {128, 64, 28.0, 28.0, 2.0}, {16, 16, 6.3, 6.3, 1.0}};
+static const GroupTile GROUP_TILES[4] = {{256, 256, 80.0, 52.0, 80.0, 14.0}, {128, 128, 43.0, 43.0, 33.0, 2.0},
+                                         {128, 64, 29.5, 29.5, 25.0, 2.0}, {16, 16, 6.3, 6.3, 6.3, 1.0}};
 
 // The tile whose rounds are shortest for a product of `rows` rows of R (contraction K) over M slots of G
-// groups. The choice follows from the host's sizes: units that the groups end in are taken as half a one
-// each. (us, large / mid / slim / few: 480 slots in 48 groups of 4096 x 7168 473 / 486 / 497 / 665; 1024 in
-// 4 of 4096 x 4096 80 / 62 / 80 / 480; 16 in 4 of 1024 x 7168 76 / 53 / 40 / 13. At most 16% from the best of
-// the four where it errs: 64 slots of 16 x 4096 x 4096 111 against 133 were it the large one.)
+// groups. The choice follows from the host's sizes: of the units that groups end in, half are taken to be one
+// more each. (us, large / mid / slim / few: 480 slots in 48 groups of 4096 x 7168 465 / 464 / 496 / 663; 1024 in
+// 4 of 4096 x 4096 77 / 52 / 81 / 482; 16 in 4 of 1024 x 7168 78 / 53 / 40 / 13.)
 static int group_plan(int64_t M, int G, int64_t rows, int64_t K, bool rkc)
 {
     const double some = (double)(M < G ? M : G);   // groups with slots, at most
@@ -225,10 +235,11 @@ static int group_plan(int64_t M, int G, int64_t rows, int64_t K, bool rkc)
     double least = 0.0;
     for (int i = 0; i < (rkc ? 4 : 3); i++) {
         const GroupTile& t = GROUP_TILES[i];
-        const double full = (double)M / t.bc + some / 2.0, units = full > some ? full : some;
+        const double full = (double)((M + t.bc - 1) / t.bc) + (some - 1.0) / 2.0, units = full > some ? full : some;
         double rounds = units * (double)((rows + t.br - 1) / t.br) / 256.0;
-        if (rounds <= 2.0) rounds = rounds <= 1.0 ? 1.0 : i == GROUP_MID ? rounds : 2.0;   // two mid tiles fit a CU side by side
-        const double us = rounds * ((M <= 128 * some ? t.half : t.full) * (double)K / 4096.0 + t.rest);
+        const double each = rounds <= 1.0 && t.alone < t.full ? t.alone : M <= 128 * some ? t.half : t.full;
+        if (rounds <= 2.0) rounds = rounds <= 1.0 ? 1.0 : i == GROUP_MID ? rounds : 2.0;
+        const double us = rounds * (each * (double)K / 4096.0 + t.rest);
         if (i == 0 || us < least) {
             best = i;
             least = us;
@@ -250,11 +261,11 @@ static bool wgrad_large(int64_t M, int G, int64_t N, int64_t K)
 }
 
 // Workgroups of a product over the slots: rows of R in tiles of br, slots in units (a group adds at
-// most one that is not full)
+// most one that is not full; two lists of them are dealt to the XCDs apart)
 static int64_t group_grid(int64_t M, int G, int64_t rows, int64_t br, int64_t unit)
 {
     const int64_t units = M / unit + G < M ? M / unit + G : M;
-    return (units * ((rows + br - 1) / br) + 7) / 8 * 8;
+    return (units * ((rows + br - 1) / br) + 7) / 8 * 8 + 8;
 }
 
 static int64_t wgrad_grid(int G, int64_t N, int64_t K, int64_t b)
@@ -277,6 +288,11 @@ static void group_launch(GroupArgs a, int64_t M, hipStream_t stream)
 {
     const int64_t nr = EPI == FFN_SWIGLU ? a.p.F : a.p.Nr, br = EPI == FFN_SWIGLU ? T::BR / 2 : T::BR;
     a.p.rtiles = (nr + br - 1) / br;
+    // Where most units are half a one, the others go first: they take twice as long (2004 slots in 32 groups,
+    // dgrad of 4096 x 1024: 137 us in the groups' order, 124 so; 4800 in 48 of 4096 x 7168: 624 / 593). Where
+    // groups have many whole units, a half one reads again what the group's others had in L2 (24000 in 48:
+    // 1461 / 1497).
+    a.apart = T::HALVES && M <= T::BC / 2 * (M < a.G ? M : a.G);
     hipLaunchKernelGGL((k_group_gemm<T, RKC, EPI, GATHER>), dim3((unsigned)group_grid(M, a.G, nr, br, T::BC)), dim3(T::THREADS), 0,
                        stream, a);
 }

@@ -380,7 +380,7 @@ PMN_DEV float wave_max(float v)
 // ---- ragged groups --------------------------------------------------------------------------
 
 // Unit t of the concatenation of per-group unit lists, where group g (slots offsets[g] ..
-// offsets[g+1]) holds ceil(size / unit) units: its group, its index inside the group and the
+// offsets[g+1]) holds count(size) units: its group, its index inside the group and the
 // group's slot range. Wavefront-parallel (lane l reads group 64c + l, a prefix sum over the lanes
 // and a ballot pick the group), so the cost does not grow with the group index. Every lane of
 // the wavefront must call it; the result is wavefront-uniform. g = -1 when t is past the end.
@@ -390,14 +390,15 @@ struct GroupUnit {
     int64_t s0, s1;     // the group's slots
 };
 
-PMN_DEV GroupUnit locate_group_unit(const int64_t* offsets, int G, int64_t t, int64_t unit)
+template <typename F>
+PMN_DEV GroupUnit locate_group(const int64_t* offsets, int G, int64_t t, F count)
 {
     const int lane = threadIdx.x & 63;
     int64_t before = 0;   // units of the groups of earlier chunks
     for (int c0 = 0; c0 < G; c0 += 64) {
         const int gl = c0 + lane;
         const int64_t a = gl < G ? offsets[gl] : 0, b = gl < G ? offsets[gl + 1] : 0;
-        const int64_t n = (b - a + unit - 1) / unit;
+        const int64_t n = count(b - a);
         int64_t cum = n;   // inclusive prefix over the lanes
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -417,6 +418,12 @@ PMN_DEV GroupUnit locate_group_unit(const int64_t* offsets, int G, int64_t t, in
         before += __shfl(cum, 63, 64);
     }
     return GroupUnit{-1, 0, 0, 0};
+}
+
+// The same with ceil(size / unit) units a group
+PMN_DEV GroupUnit locate_group_unit(const int64_t* offsets, int G, int64_t t, int64_t unit)
+{
+    return locate_group(offsets, G, t, [unit](int64_t n) { return (n + unit - 1) / unit; });
 }
 
 // ---- GEMM epilogues shared by the forward GEMMs -------------------------------------------
