@@ -14,9 +14,10 @@
 // descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
 // the same code.
 //   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
-//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured). Where both operands are KC,
-//     two stages at a time: rows of 128 bytes, chunk c at slot c ^ ((r / 2) % 8), so that a load takes whole
-//     lines of 8 rows and not halves of 16 (49152 x 4096 x 7168: 2130 us with halves, 2025 so).
+//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured). In the tiles with PAIRS, where
+//     both operands are KC or C alone is, two stages at a time: rows of 128 bytes, chunk c at slot
+//     c ^ ((r / 2) % 8), so that a load takes whole lines of 8 rows and not halves of 16 (49152 x 4096 x 7168,
+//     both KC: 2130 us with halves, 2025 so; 65536 x 7168 x 2048 in 48 groups, C alone: 1866 and 1770).
 //   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
 //     of 16 the column i of 4 k; the 32-byte pairs of chunks of row k are permuted by
 //     ((k / 8) % 2) | 2 (k % 4), so that the 4 k of 16 lanes lie in different banks (174 B/clk/CU
@@ -149,7 +150,7 @@ PMN_DEV void dma16_flat(const void* src, uint32_t lds)
 static __device__ const uint4 ffn_zeros = {0u, 0u, 0u, 0u};   // what a gathered chunk outside the operand reads
 
 // WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of two and a half or three pairs
-// of them (PAIRS, where both operands are k-contiguous)
+// of them (PAIRS, where both operands are k-contiguous; where C alone is, NST stages of R and three pairs of C)
 template <int WR_, int WC_, int RB_, int CB_, int NST_>
 struct FfnTile {
     static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
@@ -199,9 +200,12 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
 {
     constexpr int BR = T::BR, BC = T::BC, RB = T::RB, CB = T::CB, PPW = T::PPW;
     constexpr bool SWI = EPI == FFN_SWIGLU, LINES = T::PAIRS && RKC && CKC;
+    constexpr bool CLINES = T::PAIRS && CKC, ONE_PAIR = CLINES && !RKC;   // C alone by pairs of stages
     constexpr int NST = T::NST;
-    constexpr int NR = LINES ? 2 * T::RPW : T::RPW, NC = LINES ? 2 * T::CPW : T::CPW, NPC = NR + NC;   // pieces of a wavefront
-    constexpr int PROWS = LINES ? 8 : 16;   // rows of a k-contiguous operand's piece
+    constexpr int NR = LINES ? 2 * T::RPW : T::RPW, NC = CLINES ? 2 * T::CPW : T::CPW, NPC = NR + NC;   // pieces of a wavefront
+    constexpr int PR = LINES ? 8 : 16, PC = CLINES ? 8 : 16;   // rows of a k-contiguous operand's piece
+    constexpr int RSTEP = ONE_PAIR ? T::RBYTES : T::STAGE;       // bytes from a stage's R to the next one's
+    static_assert(!ONE_PAIR || NST * T::RBYTES + 3 * BC * 128 <= T::LDS, "stages of R, pairs of C");
     static_assert(!SWI || (RB % 2 == 0 && RKC), "w1 and w3 rows of a feature stand in one wavefront");
     static_assert(GATHER != GATHER_C || CKC, "C's rows are gathered where it is k-contiguous");
     static_assert(GATHER != GATHER_R || (!RKC && !CKC && EPI != FFN_PART), "R's k are gathered where it is row-contiguous, in wgrad");
@@ -224,9 +228,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     // the same lines at once: 4 to 5% at 128 x 128 (600 .. 2000 rows forward); 256 x 256 tiles are bound by
     // their MFMAs and run 1% slower with it.
     constexpr bool ROTATE = RB * CB < 16;
-    const int rotr = ROTATE ? (int)(tcol % (BR / PROWS)) : 0, rotc = ROTATE ? (int)(trow % (BC / PROWS)) : 0;
+    const int rotr = ROTATE ? (int)(tcol % (BR / PR)) : 0, rotc = ROTATE ? (int)(trow % (BC / PC)) : 0;
     auto piece_of = [&](int i) {   // piece of its operand's tile
-        return i < NR ? (wave * NR + i + rotr) % (BR / PROWS) : (wave * NC + i - NR + rotc) % (BC / PROWS);
+        return i < NR ? (wave * NR + i + rotr) % (BR / PR) : (wave * NC + i - NR + rotc) % (BC / PC);
     };
     uint32_t voff[NPC];
     int kch[NPC];
@@ -237,8 +241,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         const int q = piece_of(i);
         const int64_t ld = isr ? p.ldr : p.ldc;
         if (isr ? RKC : CKC) {
-            const int t = LINES ? q * 8 + (lane >> 3) : q * 16 + (lane >> 2);   // tile row
-            const int ch = LINES ? (lane & 7) ^ ((t >> 1) & 7) : (lane & 3) ^ ((t >> 2) & 3);
+            const bool lines = isr ? LINES : CLINES;
+            const int t = lines ? q * 8 + (lane >> 3) : q * 16 + (lane >> 2);   // tile row
+            const int ch = lines ? (lane & 7) ^ ((t >> 1) & 7) : (lane & 3) ^ ((t >> 2) & 3);
             int row = t;                                              // from the tile's first
             bool ok;
             if (SWI && isr) {
@@ -283,10 +288,12 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         uint32_t at;
         int left;         // k from the stage's first to the part's end: none where it is not positive
         uint32_t dst, dstc;   // where R's and C's pieces go
+        uint32_t atc;         // ONE_PAIR: at and left of C's pair
+        int leftc;
     };
     const uint64_t r3 = SWI ? (uint64_t)p.F * p.ldr * 2 : 0;   // from w1's rows to w3's
     constexpr bool ONE_HALF = SWI && !ROTATE && RB % T::RPW == 0;   // a wavefront's pieces of R are all of w1 or all of w3
-    auto of_w3 = [&](int i) { return SWI && ((piece_of(i) * PROWS) >> 5) % RB >= RB / 2; };
+    auto of_w3 = [&](int i) { return SWI && ((piece_of(i) * PR) >> 5) % RB >= RB / 2; };
     auto records = [&](int left, int64_t ld, int64_t at) {
         const int rows = left < 64 ? left : 64;
         return rows > 0 ? (int)((rows * (int)ld - (int)at) * 2) : 0;
@@ -300,8 +307,10 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         g.left = kend - (int)k0 - s * 32;
         g.rrec = RKC ? 0x7FFFFFFF : records(g.left, p.ldr, r0);
         g.crec = CKC ? 0x7FFFFFFF : records(g.left, p.ldc, c0);
-        g.dst = (uint32_t)(s % NST) * T::STAGE + lds0;
-        g.dstc = g.dst + T::RBYTES;
+        g.dst = (uint32_t)(s % NST) * RSTEP + lds0;
+        g.dstc = ONE_PAIR ? lds0 + NST * T::RBYTES : g.dst + T::RBYTES;
+        g.atc = g.at;
+        g.leftc = g.left;
         return g;
     };
     // the same `by` stages on; in scalar instructions few enough for the gap between two MFMAs
@@ -309,9 +318,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
         constexpr int BY = decltype(by)::value;
         g.left -= 32 * BY;
         g.at += 64 * BY;
-        g.dst += BY * T::STAGE;
-        g.dst = g.dst >= lds0 + NST * T::STAGE ? g.dst - NST * T::STAGE : g.dst;
-        g.dstc = g.dst + T::RBYTES;
+        g.dst += BY * RSTEP;
+        g.dst = g.dst >= lds0 + NST * RSTEP ? g.dst - NST * RSTEP : g.dst;
+        if (!ONE_PAIR) g.dstc = g.dst + T::RBYTES;
         if (!RKC && GATHER != GATHER_R) {
             g.r += (uint64_t)(64 * BY) * p.ldr;
             g.rrec = records(g.left, p.ldr, r0);
@@ -321,12 +330,17 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             g.crec = records(g.left, p.ldc, c0);
         }
     };
+    auto next_c = [&](Stage& g) {   // ONE_PAIR: C's next pair
+        g.atc += 128;
+        g.leftc -= 64;
+        g.dstc = g.dstc == lds0 + NST * T::RBYTES + 2 * BC * 128 ? lds0 + NST * T::RBYTES : g.dstc + BC * 128;
+    };
     auto descriptor = [](uint64_t first, int bytes) {
         return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)first), __builtin_amdgcn_readfirstlane((int)(uint32_t)(first >> 32)),
                      __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
     };
     // Piece i's lane offset in stage g: chunks past the part's end of a k-contiguous operand lie outside
-    auto lane_offset = [&](const Stage& g, int i) { return (i < NR ? RKC : CKC) && kch[i] >= g.left ? FFN_OUTSIDE : voff[i]; };
+    auto lane_offset = [&](const Stage& g, int i) { return (i < NR ? RKC : CKC) && kch[i] >= (ONE_PAIR ? g.leftc : g.left) ? FFN_OUTSIDE : voff[i]; };
     struct Index {
         uint32_t v[GATHER == GATHER_R ? T::RPW : 1];
     };
@@ -355,9 +369,9 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             dma16_flat(kch[i] >= g.left ? z : row, g.dst + piece_of(i) * 1024);
         } else if (GATHER == GATHER_C && !isr) {
             const uint8_t* z = reinterpret_cast<const uint8_t*>(&ffn_zeros);
-            dma16_flat(kch[i] >= g.left ? z : from[i - NR] + g.at, g.dstc + piece_of(i) * 1024);
+            dma16_flat(kch[i] >= (ONE_PAIR ? g.leftc : g.left) ? z : from[i - NR] + (ONE_PAIR ? g.atc : g.at), g.dstc + piece_of(i) * 1024);
         } else if (!isr) {
-            dma16_buffer(descriptor(g.c, g.crec), v, CKC ? g.at : 0u, g.dstc + piece_of(i) * 1024);
+            dma16_buffer(descriptor(g.c, g.crec), v, ONE_PAIR ? g.atc : CKC ? g.at : 0u, g.dstc + piece_of(i) * 1024);
         } else {
             dma16_buffer(descriptor(!ONE_HALF && of_w3(i) ? g.r + r3 : g.r, g.rrec), v, RKC ? g.at : 0u, g.dst + piece_of(i) * 1024);
         }
@@ -369,8 +383,8 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     // lane constants of the fragment reads
     const int swz = (l32 >> 2) & 3, swl = (l32 >> 1) & 7;
     const int g16 = lane >> 4, i16 = lane & 15, swt = (g16 >> 1) | ((i16 >> 2) << 1);
-    auto read_frag = [&](const uint8_t* base, auto kc, int width, int blk, int ks, int half) -> bf16x8 {
-        if constexpr (decltype(kc)::value && LINES) {
+    auto read_frag = [&](const uint8_t* base, auto kc, auto lines, int width, int blk, int ks, int half) -> bf16x8 {
+        if constexpr (decltype(lines)::value) {
             return *reinterpret_cast<const bf16x8*>(base + (blk * 32 + l32) * 128 + (((4 * half + 2 * ks + hh) ^ swl) << 4));
         } else if constexpr (decltype(kc)::value) {
             return *reinterpret_cast<const bf16x8*>(base + (blk * 32 + l32) * 64 + (((2 * ks + hh) ^ swz) << 4));
@@ -386,13 +400,16 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
     constexpr int NREAD = 2 * (RB + CB);   // fragments of a stage, in the order of their use
     struct Place {   // a stage's fragments
         const uint8_t *r, *c;
-        int half;    // LINES: of its pair
+        int half;    // of its pair
     };
-    auto place_of = [&](int s) { return Place{lds + (s % NST) * T::STAGE, lds + (s % NST) * T::STAGE + T::RBYTES, 0}; };
+    uint32_t pair_in = NST * T::RBYTES;   // ONE_PAIR: the pair of C that is read
+    auto place_of = [&](int s, int half) {
+        return Place{lds + (s % NST) * RSTEP, ONE_PAIR ? lds + pair_in : lds + (s % NST) * RSTEP + T::RBYTES, half};
+    };
     auto read_one = [&](const Place& at, int n, Frags& f) {
         const int ks = n / (RB + CB), b = n % (RB + CB);
-        if (b < RB) f.r[b][ks] = read_frag(at.r, std::integral_constant<bool, RKC>{}, BR * 2, wr * RB + b, ks, at.half);
-        else f.c[b - RB][ks] = read_frag(at.c, std::integral_constant<bool, CKC>{}, BC * 2, wc * CB + b - RB, ks, at.half);
+        if (b < RB) f.r[b][ks] = read_frag(at.r, std::integral_constant<bool, RKC>{}, std::integral_constant<bool, LINES>{}, BR * 2, wr * RB + b, ks, at.half);
+        else f.c[b - RB][ks] = read_frag(at.c, std::integral_constant<bool, CKC>{}, std::integral_constant<bool, CLINES>{}, BC * 2, wc * CB + b - RB, ks, at.half);
     };
 
     f32x16 acc[RB][CB];
@@ -455,6 +472,19 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
                 load_index(s + NST);
                 advance(g, one);
             }
+        } else if constexpr (ONE_PAIR) {
+            // R of stages 0 .. 3; C of pairs 0 and 1 and half of 2, as the steps before the first would load them
+            static_assert(NST == 4, "three steps and a half ahead");
+#pragma unroll
+            for (int s = 0; s < NST; s++) {
+#pragma unroll
+                for (int i = 0; i < NR; i++) issue_piece(g, i, lane_offset(g, i));
+                const int c0 = s == 2 ? NC / 2 : 0, c1 = s == 0 || s == 2 ? NC : NC / 2;
+#pragma unroll
+                for (int i = c0; i < c1; i++) issue_piece(g, NR + i, lane_offset(g, NR + i));
+                if (s == 0 || s == 2) next_c(g);
+                advance(g, one);
+            }
         } else {
 #pragma unroll
             for (int s = 0; s < NST; s++) {
@@ -464,25 +494,32 @@ PMN_DEV void ffn_tile(const FfnArgs& p, int64_t trow, int64_t tcol, int split, u
             }
         }
         wait_loads_and_barrier<(NST - 1) * LPS>();
-        read_first(place_of(0));
+        read_first(place_of(0, 0));
         if constexpr (GATHER == GATHER_R) index = read_index(NST);
         // stage v + 1 has landed and every wavefront is done reading stage v, whose slot is refilled
-        auto step = [&](int v, const Frags& cur, Frags& nxt) {
+        // (ONE_PAIR: an even step loads half of C's pair v / 2 + 2, an odd one half of the one after it, whose slot's
+        // last fragments were read in the step before)
+        auto step = [&](int v, auto second, const Frags& cur, Frags& nxt) {
+            constexpr bool odd = decltype(second)::value;
+            auto piece = [](int n) { return !ONE_PAIR || n < NR ? n : n + (odd ? 0 : NC / 2); };
             wait_loads_and_barrier<(NST - 2) * LPS>();
             const Stage h = g;   // stage v + NST
             Index ahead;
             if constexpr (GATHER == GATHER_R) ahead = read_index(v + NST + 1);
-            compute(place_of(v + 1), cur, nxt, [&](int n) { return lane_offset(h, n); }, [&](int n, uint32_t o) { issue_piece(h, n, o); },
+            if (ONE_PAIR && odd) pair_in = pair_in == NST * T::RBYTES + 2 * BC * 128 ? NST * T::RBYTES : pair_in + BC * 128;
+            compute(place_of(v + 1, odd ? 0 : 1), cur, nxt, [&](int n) { return lane_offset(h, piece(n)); },
+                    [&](int n, uint32_t o) { issue_piece(h, piece(n), o); },
                     [&](int q) {
                         if (q == LATE) advance(g, one);
+                        if (ONE_PAIR && !odd && q == LATE) next_c(g);
                         if constexpr (GATHER == GATHER_R)
                             if (q == LATE + 1) load_index(v + 2 * NST);
                     });
             if constexpr (GATHER == GATHER_R) index = ahead;
         };
         for (int v = 0; v < nst; v += 2) {     // past an odd count the second step multiplies zeros
-            step(v, f0, f1);
-            step(v + 1, f1, f0);
+            step(v, std::false_type{}, f0, f1);
+            step(v + 1, std::true_type{}, f1, f0);
         }
     } else {
         // Both operands k-contiguous: a row gives 64 bytes to a stage, half a 128-byte line. Stages go in
