@@ -162,7 +162,7 @@ struct FfnTile {
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
     static constexpr bool HALVES = RB_ * CB_ == 16;
     typedef FfnTile<WR_, WC_, RB_, CB_ / 2, NST_> Half;         // of the output rows, all of the columns
-    static constexpr bool PAIRS = RPW % 2 == 0 && CPW % 2 == 0;
+    static constexpr bool PAIRS = RPW % 2 == 0;   // of stages, where an operand is k-contiguous
     static constexpr int RING = !PAIRS ? NST * STAGE : BR == BC ? 5 * BR * 128 : 3 * (BR + BC) * 128, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");

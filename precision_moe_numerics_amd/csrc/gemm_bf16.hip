@@ -222,7 +222,7 @@ struct GroupTile {
 };
 enum { GROUP_LARGE = 0, GROUP_MID = 1, GROUP_SLIM = 2, GROUP_FEW = 3 };
 static const GroupTile GROUP_TILES[4] = {{256, 256, 80.0, 52.0, 80.0, 14.0}, {128, 128, 43.0, 43.0, 33.0, 2.0},
-                                         {128, 64, 29.5, 29.5, 25.0, 2.0}, {16, 16, 6.3, 6.3, 6.3, 1.0}};
+                                         {128, 64, 29.5, 29.5, 23.0, 2.0}, {16, 16, 6.3, 6.3, 6.3, 1.0}};
 
 // The tile whose rounds are shortest for a product of `rows` rows of R (contraction K) over M slots of G
 // groups. The choice follows from the host's sizes: of the units that groups end in, half are taken to be one
