@@ -58,9 +58,21 @@ PMN_DEV int64_t uniform64(int64_t v)
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// Item of workgroup L among n: each XCD takes 32 consecutive ones of every 256 (of what is left at the end, an
+// eighth), so that all of them work on the same few groups at a time, whose operands the last-level cache holds:
+// tiles of an XCD drift apart where some are halves, and miss its L2 (65536 slots in 48 groups of 4096 x 7168,
+// each XCD on an eighth of all items 3326 us, so 3229; in blocks of 512 and 1024 1 and 2% slower). Negative past
+// the last.
+PMN_DEV int64_t group_item_of(int64_t n, int64_t L)
+{
+    const int64_t b = L >> 8, r = L & 255, left = n - (b << 8);
+    const int64_t per = left < 256 ? (left + 7) >> 3 : 32, i = (r & 7) * per + (r >> 3);
+    return (r >> 3) >= per || i >= left ? -1 : (b << 8) + i;
+}
+
 // Workgroup L's tile of a product over the groups' slots: units of `unit` slots, a.p.rtiles tiles
-// of R each. Consecutive tiles of a group run on one XCD in bands of 8 tiles of R, so that they share
-// panels of both operands in its L2. With a.apart the units of at most unit / 2 slots run after all others.
+// of R each. Consecutive tiles of a group, in bands of 8 tiles of R, run on one XCD and share panels of both
+// operands in its L2. With a.apart the units of at most unit / 2 slots run after all others.
 // False past the last.
 template <bool GATHER>
 PMN_DEV bool group_tile(const GroupArgs& a, int64_t L, int64_t unit, FfnArgs& p, int64_t& trow, int64_t& tcol)
@@ -71,7 +83,7 @@ PMN_DEV bool group_tile(const GroupArgs& a, int64_t L, int64_t unit, FfnArgs& p,
     const int64_t n = uniform64(group_units(a.offsets, a.G, firsts)) * a.p.rtiles, per = (n + 7) >> 3;
     const bool late = (L >> 3) >= per;
     if (late && !a.apart) return false;
-    const int64_t i = late ? ffn_item_of(uniform64(group_units(a.offsets, a.G, others)) * a.p.rtiles, L - per * 8) : ffn_item_of(n, L);
+    const int64_t i = late ? ffn_item_of(uniform64(group_units(a.offsets, a.G, others)) * a.p.rtiles, L - per * 8) : group_item_of(n, L);
     if (i < 0) return false;
     const int64_t u = i / a.p.rtiles;
     const GroupUnit w = late ? locate_group(a.offsets, a.G, u, others) : locate_group(a.offsets, a.G, u, firsts);
