@@ -640,8 +640,9 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise PmnError(f"{name} must be on the GPU")
-    if dev != torch.cuda.current_device():
-        raise PmnError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    current = torch._C._cuda_getDevice()   # torch.cuda.current_device() without its check that CUDA is up: t is on it
+    if dev != current:
+        raise PmnError(f"{name} is on cuda:{dev}, the current device is cuda:{current}")
     return dev
 
 
@@ -939,7 +940,8 @@ def moe_gemv_nvfp4(x: torch.Tensor, wq: NVFP4, N: int, ids: Optional[torch.Tenso
     dtype = torch.float32 if epilogue == EPI_F32 else torch.bfloat16
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
-    _tensor(out, shape, dtype, "out")
+    else:
+        _tensor(out, shape, dtype, "out")
     if gates is not None:
         need = _lib.moe_gemv_nvfp4_workspace_size(T, k, N, 1)
         workspace = _workspace(workspace, need, dev) if need or workspace is not None else None
@@ -978,7 +980,8 @@ def moe_combine_rows_fwd(y: torch.Tensor, slot_of: torch.Tensor, gates: Optional
     at = _device_of(slot_of, "slot_of")
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype, device=y.device)
-    _tensor(out, (T, H), out_dtype, "out")
+    else:
+        _tensor(out, (T, H), out_dtype, "out")
     _check(_lib.moe_combine_rows_fwd(
         _device_ptr(y, at, "y"), ycode, M, H, _device_ptr(slot_of, at, "slot_of"), _device_ptr(gates, at, "gates"),
         _device_ptr(add, at, "add"), T, k, _device_ptr(out, at, "out"),
