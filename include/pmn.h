@@ -466,10 +466,11 @@ int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gath
  * dh13 bf16 [M x 2K] = da h3 silu'(h1) | da silu(h1), formed from the fp32 da. Then x may be NULL: wgrad takes
  * silu(h1) h3, rounded to bf16, from h13. With h13: DGRAD set, no gather, da_dtype bf16 (PMN_EINVAL).
  * Sizes and alignment as the forward. Workspace (16-byte aligned, at least
- * moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, from_h13) bytes, PMN_EWORKSPACE; no initialization)
- * holds the rebuilt activation where x is NULL (from_h13 1); else nothing is needed.
+ * moe_grouped_gemm_bwd_bf16_workspace_size(...) bytes, PMN_EWORKSPACE; no initialization) holds the rebuilt
+ * activation where x is NULL (from_h13 1), and the parts of weight gradients of few and small matrices over many
+ * slots; the size is 0 where nothing is needed.
  */
-size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int from_h13);
+size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int G, int64_t N, int64_t K, int flags, int from_h13);
 int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, const int32_t* gather, const void* w,
                               const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, int flags,
                               const void* h13, void* da, int da_dtype, void* db, int db_dtype, void* workspace,

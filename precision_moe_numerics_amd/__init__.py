@@ -58,7 +58,7 @@ _SIGS = {
     "adamw_table_build": (I32, [P, I32, I32, P, SZ, P]),
     "adamw_step": (I32, [P, I64, I32, F64, F64, F64, F64, I64, P, P, P, U64, U32, P]),
     "moe_grouped_gemm_fwd_bf16": (I32, [P, I64, P, P, P, I32, I64, I64, I64, I32, P, P, P]),
-    "moe_grouped_gemm_bwd_bf16_workspace_size": (SZ, [I64, I64, I32, I32]),
+    "moe_grouped_gemm_bwd_bf16_workspace_size": (SZ, [I64, I32, I64, I64, I32, I32]),
     "moe_grouped_gemm_bwd_bf16": (I32, [P, P, I64, P, P, P, I32, I64, I64, I64, I32, P, P, I32, P, I32, P, SZ, P]),
     "moe_gemv_nvfp4_workspace_size": (SZ, [I64, I32, I64, I32]),
     "moe_gemv_nvfp4": (I32, [P, I32, P, P, P, I64, P, P, P, I64, I32, I32, I64, I64, I32, P, P, SZ, P]),
@@ -846,8 +846,8 @@ def moe_grouped_gemm_fwd_bf16(x: torch.Tensor, w: torch.Tensor, offsets: torch.T
     return (out, out_aux) if swiglu else out
 
 
-def moe_grouped_gemm_bwd_bf16_workspace_size(M: int, K: int, flags: int, from_h13: bool) -> int:
-    return _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, int(from_h13))
+def moe_grouped_gemm_bwd_bf16_workspace_size(M: int, G: int, N: int, K: int, flags: int, from_h13: bool) -> int:
+    return _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, G, N, K, flags, int(from_h13))
 
 
 def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor, offsets: torch.Tensor,
@@ -885,7 +885,7 @@ def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: to
         _tensor(db, (G * N, K), db_dtype, "db")
     elif wgrad:
         db = torch.empty((G * N, K), dtype=db_dtype, device=dev)
-    need = _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, 1) if x is None else 0
+    need = _lib.moe_grouped_gemm_bwd_bf16_workspace_size(M, G, N, K, flags, x is None and h13 is not None)
     workspace = _workspace(workspace, need, dev) if need or workspace is not None else None
     _check(_lib.moe_grouped_gemm_bwd_bf16(
         _device_ptr(dy, at, "dy"), _device_ptr(x, at, "x"), 0 if x is None else x.shape[0],

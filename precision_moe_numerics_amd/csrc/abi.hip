@@ -599,9 +599,10 @@ int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gath
                                              hs(stream)));
 }
 
-size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int64_t K, int flags, int from_h13)
+size_t moe_grouped_gemm_bwd_bf16_workspace_size(int64_t M, int G, int64_t N, int64_t K, int flags, int from_h13)
 {
-    return M <= 0 || K <= 0 || !(flags & PMN_BWD_WGRAD) || !from_h13 ? 0 : round256((size_t)(M * K) * 2);
+    if (!(flags & PMN_BWD_WGRAD) || bad_group_shape(M, G, N, K, M, false)) return 0;
+    return (from_h13 ? round256((size_t)(M * K) * 2) : 0) + pmn::group_wgrad_part_bytes(M, G, N, K);
 }
 
 int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, const int32_t* gather, const void* w,
@@ -620,7 +621,7 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
     const bool rebuild = wgrad && !x && h13;
     if (!offsets || (wgrad && !db)) return PMN_EINVAL;
     if (M > 0 && (!dy || (dgrad && (!w || !da)) || (wgrad && !x && !rebuild))) return PMN_EINVAL;
-    const size_t need = moe_grouped_gemm_bwd_bf16_workspace_size(M, K, flags, rebuild);
+    const size_t need = moe_grouped_gemm_bwd_bf16_workspace_size(M, G, N, K, flags, rebuild);
     if (need > 0 && (!workspace || workspace_bytes < need)) return PMN_EWORKSPACE;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(h13, 16) || !aligned(gather, 4) ||
         !aligned(offsets, 8) || (dgrad && !aligned(da, 16)) || (wgrad && !aligned(db, 16)) ||
@@ -628,10 +629,11 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
         return PMN_EALIGN;
     if (M == 0 && !wgrad) return PMN_OK;
     uint16_t* const act = rebuild ? static_cast<uint16_t*>(workspace) : nullptr;
+    float* const part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (rebuild ? round256((size_t)(M * K) * 2) : 0));
     return status(pmn::launch_group_bwd_bf16(
         static_cast<const uint16_t*>(dy), rebuild ? act : static_cast<const uint16_t*>(x), gather,
         static_cast<const uint16_t*>(w), offsets, G, M, N, K, static_cast<const uint16_t*>(h13), dgrad ? da : nullptr,
-        da_dtype == PMN_DTYPE_F32, act, wgrad ? db : nullptr, db_dtype == PMN_DTYPE_F32, hs(stream)));
+        da_dtype == PMN_DTYPE_F32, act, wgrad ? db : nullptr, db_dtype == PMN_DTYPE_F32, part, hs(stream)));
 }
 
 static bool bad_gemv_shape(int64_t T, int k, int G, int64_t N, int64_t K)

@@ -24,6 +24,7 @@ struct GroupArgs {
     int out_bytes;
     int64_t out2_width;
     bool apart;               // half tiles run after the whole ones
+    int splits;               // parts of a group's slots in wgrad
 };
 
 // Moves p to group g, whose slots are s0 .. s1
@@ -114,25 +115,55 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_gro
 }
 
 // dW: p.Nr = K columns, p.Nc = N rows, contraction over the group's slots. The tiles of each group are
-// dealt to all XCDs in runs, as the groups differ in length.
+// dealt to all XCDs in runs, as the groups differ in length. With a.splits the slots of each group go in as many
+// parts (multiples of 32), whose sums stand one after another in p.out for k_group_wgrad_sum.
 template <typename T, int EPI, bool GATHER>
 __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_group_wgrad(GroupArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
     if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));
     const int64_t tiles = a.p.rtiles * a.p.ctiles, per = (tiles + 7) >> 3;
-    const int64_t j = blockIdx.x >> 3, g = j / per, i = (blockIdx.x & 7) * per + (j - g * per);
-    if (i >= tiles || g >= a.G) return;
-    const int64_t s0 = uniform64(a.offsets[g]), s1 = uniform64(a.offsets[g + 1]);
+    const int64_t j = blockIdx.x >> 3, gs = j / per, i = (blockIdx.x & 7) * per + (j - gs * per);
+    const int64_t part = gs / a.G, g = gs - part * a.G;
+    if (i >= tiles || part >= a.splits) return;
+    int64_t s0 = uniform64(a.offsets[g]), s1 = uniform64(a.offsets[g + 1]);
+    if (a.splits > 1) {
+        const int64_t n = s1 - s0, stages = (n + 31) >> 5, k1 = stages * (part + 1) / a.splits * 32;
+        s1 = s0 + (k1 < n ? k1 : n);
+        s0 += stages * part / a.splits * 32;
+    }
     FfnArgs p = a.p;
     if (GATHER) p.gather += s0;
     else p.r += s0 * p.ldr;
     p.c += s0 * p.ldc;
     p.K = s1 - s0;
-    p.out = static_cast<uint8_t*>(p.out) + g * p.Nc * p.Nr * a.out_bytes;
+    p.out = static_cast<uint8_t*>(p.out) + gs * p.Nc * p.Nr * a.out_bytes;
     int64_t trow, tcol;
     ffn_tile_at(p, i, trow, tcol);
     ffn_tile<T, false, false, EPI, GATHER ? GATHER_R : GATHER_NONE>(p, trow, tcol, 0, lds);
+}
+
+// The parts' sums in their order, n8 times 8 values
+template <bool F32>
+__global__ __launch_bounds__(256) void k_group_wgrad_sum(const float* __restrict__ part, int splits, int64_t n8, void* __restrict__ out)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n8) return;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; s++) {
+        const float4* q = reinterpret_cast<const float4*>(part + (s * n8 + i) * 8);
+        const float4 a = q[0], b = q[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    if (F32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + i * 8);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i * 8) =
+            make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+    }
 }
 
 // Forward for few slots a group: units of 16 slots, the weights straight to registers. A workgroup holds
@@ -272,6 +303,35 @@ static bool wgrad_large(int64_t M, int G, int64_t N, int64_t K)
     return us(256, 80.0, 8.0) <= us(128, 36.0, 2.0);
 }
 
+// Parts of each group's slots in wgrad, where the 128 x 128 tiles of all groups leave half of the CUs idle: a tile
+// takes 36 us for 4096 slots, the parts are written and read at some 3 TB/s and their sum takes 5 us more; as many
+// parts of 256 slots or more as make that least, if it gains 4 us. (With the data gradient: one
+// group of 304 x 960 from 4767 slots 54 us in one part, 31 in seven; two of 512 x 1024 from 8192 51, 42 in four;
+// without the bound two parts of 4 x 512 x 512 from 4096 slots took 23 us, one 21.)
+static int wgrad_splits(int64_t M, int G, int64_t N, int64_t K)
+{
+    const int64_t tiles = G * ((N + 127) / 128) * ((K + 127) / 128);
+    if (tiles > 128 || wgrad_large(M, G, N, K)) return 1;
+    const double whole = (double)M / G * (36.0 / 4096.0), part = (double)(G * N * K) * 8.0 / 3e6;
+    const int64_t most = M / G / 256 < 512 / tiles ? M / G / 256 : 512 / tiles;
+    int best = 1;
+    double least = whole - 4.0;
+    for (int s = 2; s <= most && s <= 32; s++) {
+        const double us = whole / s + s * part + 5.0;
+        if (us < least) {
+            best = s;
+            least = us;
+        }
+    }
+    return best;
+}
+
+size_t group_wgrad_part_bytes(int64_t M, int G, int64_t N, int64_t K)
+{
+    const int s = wgrad_splits(M, G, N, K);
+    return s > 1 ? (size_t)s * G * N * K * 4 : 0;
+}
+
 // Workgroups of a product over the slots: rows of R in tiles of br, slots in units (a group adds at
 // most one that is not full; two lists of them are dealt to the XCDs apart)
 static int64_t group_grid(int64_t M, int G, int64_t rows, int64_t br, int64_t unit)
@@ -347,10 +407,11 @@ hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const
     return hipGetLastError();
 }
 
-// da (or with h13: dh13 [M x 2K], and a [M x K] where it is not null) and dw, each where not null
+// da (or with h13: dh13 [M x 2K], and a [M x K] where it is not null) and dw, each where not null; part: of
+// group_wgrad_part_bytes
 hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
                                  const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
-                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32,
+                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32, float* part,
                                  hipStream_t stream)
 {
     if (da && M > 0) {
@@ -360,13 +421,16 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
         else group_gemm<false, FFN_BF16, false>(a, M, stream);
     }
     if (dw) {
-        GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, dw, nullptr, nullptr, 0}, offsets, G, 0, 0, dw_f32 ? 4 : 2, 0};
+        const int splits = wgrad_splits(M, G, N, K);
+        const bool parts = splits > 1, f32 = dw_f32 || parts;
+        GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, parts ? part : dw, nullptr, nullptr, 0}, offsets, G, 0, 0, f32 ? 4 : 2, 0};
         a.p.gather = gather;
+        a.splits = splits;
         auto run = [&](auto tile, auto epi) {
             typedef decltype(tile) T;
             a.p.rtiles = (K + T::BR - 1) / T::BR;
             a.p.ctiles = (N + T::BC - 1) / T::BC;
-            const dim3 grid((unsigned)wgrad_grid(G, N, K, T::BR)), block(T::THREADS);
+            const dim3 grid((unsigned)(wgrad_grid(G, N, K, T::BR) * splits)), block(T::THREADS);
             if (gather) hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, true>), grid, block, 0, stream, a);
             else hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, false>), grid, block, 0, stream, a);
         };
@@ -376,8 +440,14 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
             if (dw_f32) run(GroupLarge{}, F32{});
             else run(GroupLarge{}, BF16{});
         } else {
-            if (dw_f32) run(GroupMid{}, F32{});
+            if (f32) run(GroupMid{}, F32{});
             else run(GroupMid{}, BF16{});
+        }
+        if (parts) {
+            const int64_t n8 = G * N * K / 8;
+            const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
+            if (dw_f32) hipLaunchKernelGGL(k_group_wgrad_sum<true>, grid, block, 0, stream, part, splits, n8, dw);
+            else hipLaunchKernelGGL(k_group_wgrad_sum<false>, grid, block, 0, stream, part, splits, n8, dw);
         }
     }
     return hipGetLastError();

@@ -172,8 +172,9 @@ hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const
 // da (with h13: dh13 [M x 2K], and a [M x K] into act where it is not null) and dw, each where not null
 hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const int32_t* gather, const uint16_t* w,
                                  const int64_t* offsets, int G, int64_t M, int64_t N, int64_t K, const uint16_t* h13,
-                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32,
+                                 void* da, bool da_f32, uint16_t* act, void* dw, bool dw_f32, float* part,
                                  hipStream_t stream);
+size_t group_wgrad_part_bytes(int64_t M, int G, int64_t N, int64_t K);   // what wgrad needs beside its operands
 
 int gemv_most_pairs();
 // NVFP4 weights [G*N x K] times the rows of every pair of a token and an expert (x [T x K], per_pair: [T*k x K]):

@@ -133,6 +133,61 @@ def test_backward(P, counts, N, K, tokens):
     within(w16, dw, edw, "dw bf16")
 
 
+# (a sum in parts rounds a value no more often than in one)
+@pytest.mark.parametrize("counts,N,K,tokens", [([4767], 304, 960, 681), ([9000, 0, 5, 6000], 136, 264, 0), ([1, 33, 6000], 72, 136, 50),
+                                               ([2500], 8, 8, 0), ([20000, 13000], 48, 40, 3000), ([2100] * 20, 128, 128, 0)])
+def test_weight_gradients_in_parts(P, counts, N, K, tokens):
+    """Few and small matrices over many slots: the contraction is split, also in replays that share a workspace."""
+    c = case(counts, N, K, N + K + 7, tokens)
+    M, G = c["M"], c["G"]
+    need = P.moe_grouped_gemm_bwd_bf16_workspace_size(M, G, N, K, P.BWD_WGRAD, False)
+    assert need >= 2 * G * N * K * 4
+    _, _, dw, edw = ref_bwd(c)
+    args = (c["dy"], c["x"], c["w"], c["off"], M, N)
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+    for dt in (torch.float32, torch.bfloat16):
+        _, got = P.moe_grouped_gemm_bwd_bf16(*args, flags=P.BWD_WGRAD, gather=c["gather"], db_dtype=dt, workspace=ws[:need])
+        within(got, dw, edw, f"dw {dt}")
+        _, own = P.moe_grouped_gemm_bwd_bf16(*args, gather=c["gather"], db_dtype=dt)
+        assert torch.equal(got, own)
+    assert (ws[need:] == 0xFF).all()
+    with pytest.raises(P.PmnError):
+        P.moe_grouped_gemm_bwd_bf16(*args, gather=c["gather"], workspace=ws[:need - 1])
+    run = lambda: P.moe_grouped_gemm_bwd_bf16(*args, flags=P.BWD_WGRAD, gather=c["gather"], workspace=ws[:need])[1]  # noqa: E731
+    graphs, held = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append(run())
+        graphs.append(graph)
+    for r in range(3):
+        c["dy"].copy_(mk((M, N), 1.0, 60 + r))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want, h) for h in held), r
+
+
+@pytest.mark.parametrize("counts,N,K", [([6000, 0, 1700], 64, 136), ([3000], 40, 64)])
+def test_weight_gradients_in_parts_of_h13(P, counts, N, K):
+    c = case(counts, N, K, 71)
+    M = c["M"]
+    h13 = mk((M, 2 * K), 1.2, 72)
+    assert P.moe_grouped_gemm_bwd_bf16_workspace_size(M, c["G"], N, K, 3, True) > M * K * 2 + 512
+    dh, dw = P.moe_grouped_gemm_bwd_bf16(c["dy"], None, c["w"], c["off"], M, N, h13=h13)
+    h1, h3 = h13.double().chunk(2, 1)
+    act = h1 * torch.sigmoid(h1) * h3
+    ea = (B + 16 * U * (1 + h1.abs())) * 1.02 * act.abs()
+    for g, a, b, _ in groups(c):
+        dy = c["dy"][a:b].double()
+        within(dw[g * N:(g + 1) * N], dy.t() @ act[a:b], dy.abs().t() @ ea[a:b] + 1.02 * (b - a + 2) * U * (dy.abs().t() @ act[a:b].abs()),
+               f"dw, group {g}")
+    only, _ = P.moe_grouped_gemm_bwd_bf16(c["dy"], None, c["w"], c["off"], M, N, flags=P.BWD_DGRAD, h13=h13)
+    assert torch.equal(only, dh)
+
+
 @pytest.mark.parametrize("counts,N,K", [(c[0], c[1], c[2]) for c in CASES], ids=IDS)
 def test_backward_through_swiglu(P, counts, N, K):
     """With h13 the gradient is dh13; without x the activation is taken from h13."""

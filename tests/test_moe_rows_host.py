@@ -35,8 +35,13 @@ def test_grouped_forward_refusals(lib):
 
 def test_grouped_backward_refusals(lib):
     size = lib.moe_grouped_gemm_bwd_bf16_workspace_size
-    assert size(8, 64, 3, 0) == 0 and size(8, 64, 1, 1) == 0 and size(8, 64, 2, 1) >= 8 * 64 * 2 and size(0, 64, 3, 1) == 0
-    n = size(8, 64, 3, 1)
+    assert size(8, 2, 64, 64, 3, 0) == 0 and size(8, 2, 64, 64, 1, 1) == 0 and size(0, 2, 64, 64, 3, 1) == 0
+    assert size(8, 2, 64, 64, 2, 1) >= 8 * 64 * 2 and size(-1, 2, 64, 64, 3, 1) == 0 and size(8, 0, 64, 64, 3, 1) == 0
+    n = size(8, 2, 64, 64, 3, 1)
+    # few and small matrices over many slots: the parts' sums, at least two
+    few = size(4096, 2, 64, 64, 2, 0)
+    assert few >= 2 * 2 * 64 * 64 * 4 and size(4096, 2, 64, 64, 2, 1) == few + 4096 * 64 * 2
+    assert size(4096, 2, 64, 64, 1, 0) == 0 and size(65536, 48, 4096, 4096, 3, 0) == 0
 
     def f(dy=FAKE, x=FAKE, rows=8, gather=None, w=FAKE, off=FAKE, G=2, M=8, N=64, K=64, flags=3, h13=None, da=FAKE, dat=0,
           db=FAKE, dbt=1, ws=None, nb=0):
@@ -49,6 +54,8 @@ def test_grouped_backward_refusals(lib):
     for k in ("dy", "x", "w", "off", "da", "db"):
         assert f(**{k: None}) == EINVAL, k
     assert f(x=None, h13=FAKE) == EWS and f(x=None, h13=FAKE, ws=FAKE, nb=n - 1) == EWS
+    assert f(M=4096, rows=4096) == EWS and f(M=4096, rows=4096, ws=FAKE, nb=few - 1) == EWS
+    assert f(M=4096, rows=4096, ws=ODD, nb=few) == EALIGN
     for k in ("dy", "x", "w", "h13", "da", "db"):
         assert f(**{k: ODD}) == EALIGN, k
     assert f(x=None, h13=FAKE, ws=ODD, nb=n) == EALIGN and f(gather=C.c_void_p(0x1002)) == EALIGN
