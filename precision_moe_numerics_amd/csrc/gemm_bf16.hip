@@ -115,19 +115,20 @@ __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_gro
 }
 
 // dW: p.Nr = K columns, p.Nc = N rows, contraction over the group's slots. The tiles of each group are
-// dealt to all XCDs in runs, as the groups differ in length. With a.splits the slots of each group go in as many
+// dealt to all XCDs in runs, as the groups differ in length. With SPLIT the slots of each group go in a.splits
 // parts (multiples of 32), whose sums stand one after another in p.out for k_group_wgrad_sum.
-template <typename T, int EPI, bool GATHER>
+template <typename T, int EPI, bool GATHER, bool SPLIT>
 __global__ __launch_bounds__(T::THREADS, T::RB * T::CB == 16 ? 1 : 2) void k_group_wgrad(GroupArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
     if (T::RB * T::CB == 16) asm volatile("; agpr in use %0" ::"a"(0));
     const int64_t tiles = a.p.rtiles * a.p.ctiles, per = (tiles + 7) >> 3;
     const int64_t j = blockIdx.x >> 3, gs = j / per, i = (blockIdx.x & 7) * per + (j - gs * per);
-    const int64_t part = gs / a.G, g = gs - part * a.G;
-    if (i >= tiles || part >= a.splits) return;
+    if (i >= tiles || gs >= (SPLIT ? (int64_t)a.G * a.splits : a.G)) return;
+    const int part = SPLIT ? (int)gs / a.G : 0;
+    const int64_t g = SPLIT ? gs - (int64_t)part * a.G : gs;
     int64_t s0 = uniform64(a.offsets[g]), s1 = uniform64(a.offsets[g + 1]);
-    if (a.splits > 1) {
+    if (SPLIT) {
         const int64_t n = s1 - s0, stages = (n + 31) >> 5, k1 = stages * (part + 1) / a.splits * 32;
         s1 = s0 + (k1 < n ? k1 : n);
         s0 += stages * part / a.splits * 32;
@@ -422,28 +423,29 @@ hipError_t launch_group_bwd_bf16(const uint16_t* dy, const uint16_t* x, const in
     }
     if (dw) {
         const int splits = wgrad_splits(M, G, N, K);
-        const bool parts = splits > 1, f32 = dw_f32 || parts;
-        GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, parts ? part : dw, nullptr, nullptr, 0}, offsets, G, 0, 0, f32 ? 4 : 2, 0};
+        const bool parts = splits > 1;
+        GroupArgs a{FfnArgs{x, dy, K, N, K, N, 0, parts ? part : dw, nullptr, nullptr, 0}, offsets, G, 0, 0, parts || dw_f32 ? 4 : 2, 0};
         a.p.gather = gather;
         a.splits = splits;
-        auto run = [&](auto tile, auto epi) {
+        auto run = [&](auto tile, auto epi, auto split) {
             typedef decltype(tile) T;
+            constexpr bool S = decltype(split)::value;
             a.p.rtiles = (K + T::BR - 1) / T::BR;
             a.p.ctiles = (N + T::BC - 1) / T::BC;
             const dim3 grid((unsigned)(wgrad_grid(G, N, K, T::BR) * splits)), block(T::THREADS);
-            if (gather) hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, true>), grid, block, 0, stream, a);
-            else hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, false>), grid, block, 0, stream, a);
+            if (gather) hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, true, S>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((k_group_wgrad<T, decltype(epi)::value, false, S>), grid, block, 0, stream, a);
         };
         typedef std::integral_constant<int, FFN_F32> F32;
         typedef std::integral_constant<int, FFN_BF16> BF16;
         if (wgrad_large(M, G, N, K)) {
-            if (dw_f32) run(GroupLarge{}, F32{});
-            else run(GroupLarge{}, BF16{});
+            if (dw_f32) run(GroupLarge{}, F32{}, std::false_type{});
+            else run(GroupLarge{}, BF16{}, std::false_type{});
+        } else if (!parts) {
+            if (dw_f32) run(GroupMid{}, F32{}, std::false_type{});
+            else run(GroupMid{}, BF16{}, std::false_type{});
         } else {
-            if (f32) run(GroupMid{}, F32{});
-            else run(GroupMid{}, BF16{});
-        }
-        if (parts) {
+            run(GroupMid{}, F32{}, std::true_type{});
             const int64_t n8 = G * N * K / 8;
             const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
             if (dw_f32) hipLaunchKernelGGL(k_group_wgrad_sum<true>, grid, block, 0, stream, part, splits, n8, dw);
