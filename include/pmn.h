@@ -524,6 +524,14 @@ int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_
                          const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy, float* dgates,
                          pmn_stream_t stream);
 
+/*
+ * Zeros to the rows of x [M x H] (x_dtype) that no slot of slot_of [T x k] names: those that moe_combine_rows_bwd
+ * leaves, before or after it, where dy is new memory and pairs may be without a slot. The other rows are not
+ * touched, and a slot may stand several times. Sizes and alignment as above; T == 0: all rows.
+ */
+int moe_rows_zero_unnamed(void* x, int x_dtype, int64_t M, int64_t H, const int32_t* slot_of, int64_t T, int k,
+                          pmn_stream_t stream);
+
 /* ------------------------------------------------------------------------------------------ */
 /* Checking the device index contract (a debugging aid for callers; no other call runs it).   */
 /* ------------------------------------------------------------------------------------------ */

@@ -716,6 +716,17 @@ int moe_combine_rows_bwd(const void* dout, int dout_dtype, const void* y, int y_
                                                slot_of, gates, T, k, dy, dgates, hs(stream)));
 }
 
+int moe_rows_zero_unnamed(void* x, int x_dtype, int64_t M, int64_t H, const int32_t* slot_of, int64_t T, int k,
+                          pmn_stream_t stream)
+{
+    if (bad_dtype(x_dtype)) return PMN_EINVAL;
+    if (bad_rows_shape(M, H, T, k)) return PMN_ESHAPE;
+    if (M == 0 || H == 0) return PMN_OK;
+    if (!x || (T > 0 && !slot_of)) return PMN_EINVAL;
+    if (!aligned(x, 16) || !aligned(slot_of, 4)) return PMN_EALIGN;
+    return status(pmn::launch_zero_unnamed(slot_of, T * k, M, H * (x_dtype == PMN_DTYPE_F32 ? 4 : 2), x, hs(stream)));
+}
+
 // a chunk has 256 threads, and a launch fewer than 2^32
 constexpr int64_t ADAMW_MOST_CHUNKS = (int64_t)1 << 24;
 static int64_t adamw_chunks_of(int64_t n) { return n <= 0 ? 0 : (n + pmn::adamw_chunk() - 1) / pmn::adamw_chunk(); }

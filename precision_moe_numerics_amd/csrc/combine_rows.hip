@@ -6,7 +6,8 @@
 //
 // Forward: a thread holds 8 consecutive values of a token's row and has up to 8 slots' words on the way.
 // Backward: a workgroup takes a token, holds each word of dout for 8 slots at a time and sums their dot
-// products side by side, so that their wavefronts' sums are joined once.
+// products side by side, so that their wavefronts' sums are joined once. Rows of a new dy that no pair names
+// get zeros from a launch of their own, which reads slot_of and writes those rows alone.
 #include "pmn_dev.hpp"
 #include "pmn_kernels.hpp"
 
@@ -185,6 +186,49 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const void* __restrict
     }
 }
 
+// Zeros to the rows of x (`words` 16-byte words each) that no pair names. A workgroup marks which of its `per` rows
+// are named as bits in LDS, over all pairs, so that nothing but slot_of is read and no memory is shared. Bound by
+// a compare and a branch for each pair, in every workgroup: 131072 pairs 12 us where all rows are named (zeros to
+// 1 GB of rows beforehand: 156).
+__global__ __launch_bounds__(1024) void k_zero_unnamed(const int32_t* __restrict__ slot_of, int64_t pairs, int64_t M,
+                                                       int64_t words, int per, uint4* __restrict__ x)
+{
+    extern __shared__ uint32_t named[];
+    const int64_t r0 = (int64_t)blockIdx.x * per;
+    const uint32_t n = (uint32_t)(M - r0 < per ? M - r0 : per);
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (uint32_t i = tid; i < (n + 31) / 32; i += 1024) named[i] = 0;
+    __syncthreads();
+    auto mark = [&](int32_t s) {   // M < 2^31: what is negative lies past every row
+        const uint32_t d = (uint32_t)s - (uint32_t)r0;
+        if (d < n) atomicOr(&named[d >> 5], 1u << (d & 31));
+    };
+    const int64_t quads = reinterpret_cast<uintptr_t>(slot_of) % 16 == 0 ? pairs >> 2 : 0;
+    constexpr int AHEAD = 8;   // loads of a thread on their way
+    for (int64_t q0 = tid; q0 < quads; q0 += AHEAD * 1024) {
+        int4 s[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++) {
+            const int64_t q = q0 + i * 1024;
+            s[i] = reinterpret_cast<const int4*>(slot_of)[q < quads ? q : q0];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++) {
+            mark(s[i].x);
+            mark(s[i].y);
+            mark(s[i].z);
+            mark(s[i].w);
+        }
+    }
+    for (int64_t q = 4 * quads + tid; q < pairs; q += 1024) mark(slot_of[q]);
+    __syncthreads();
+    for (uint32_t r = tid >> 6; r < n; r += 16) {
+        if (named[r >> 5] >> (r & 31) & 1u) continue;
+        uint4* const row = x + (r0 + r) * words;
+        for (int64_t h = lane; h < words; h += 64) row[h] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 // Threads for rows of H values, 8 a thread: up to 256
 static int row_threads(int64_t H) { return H >= 1024 ? 256 : H >= 512 ? 128 : 64; }
 
@@ -233,6 +277,17 @@ hipError_t launch_combine_rows_bwd(const void* dout, bool d_f32, const void* y, 
         else PMN_ROWS(false, false);
     }
 #undef PMN_ROWS
+    return hipGetLastError();
+}
+
+hipError_t launch_zero_unnamed(const int32_t* slot_of, int64_t pairs, int64_t M, int64_t row_bytes, void* x,
+                               hipStream_t stream)
+{
+    // a workgroup a CU, of 2^18 rows (32 KB of bits) at most
+    const int64_t even = (M + 255) / 256, most = (int64_t)1 << 18;
+    const int per = (int)((even < most ? even : most) + 31) / 32 * 32;
+    hipLaunchKernelGGL(k_zero_unnamed, dim3((unsigned)((M + per - 1) / per)), dim3(1024), per / 8, stream, slot_of, pairs, M,
+                       row_bytes / 16, per, static_cast<uint4*>(x));
     return hipGetLastError();
 }
 

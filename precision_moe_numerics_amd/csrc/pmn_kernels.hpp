@@ -189,6 +189,9 @@ hipError_t launch_combine_rows(const void* y, bool y_f32, int64_t M, int64_t H, 
 hipError_t launch_combine_rows_bwd(const void* dout, bool d_f32, const void* y, bool y_f32, int64_t M, int64_t H,
                                    const int32_t* slot_of, const float* gates, int64_t T, int k, void* dy,
                                    float* dgates, hipStream_t stream);
+// zeros to the rows of x [M rows of row_bytes, a multiple of 16] that none of the pairs' slots names
+hipError_t launch_zero_unnamed(const int32_t* slot_of, int64_t pairs, int64_t M, int64_t row_bytes, void* x,
+                               hipStream_t stream);
 
 // The AdamW table on the device: this header, `count` entries, `chunks` chunk records.
 constexpr uint32_t ADAMW_MAGIC = 0x57414450u;
