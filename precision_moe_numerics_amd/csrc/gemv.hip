@@ -14,7 +14,7 @@
 // depend on the launch.
 //
 // Up to two pairs (one decoded token): codes become bf16 exactly in one conversion for two, v_dot2_f32_bf16
-// multiplies them with x from LDS, and a block's sum of 16 is multiplied by its scale once: 36 vector
+// multiplies them with x from LDS, and a block's sum of 16 is multiplied by its scale once: 40 vector
 // instructions for 32 weights and one pair. More pairs: fp4 * e4m3 has at most 6 significant bits and is exact
 // in bf16 (two conversions and two products for two weights), for v_mfma_f32_16x16x32_bf16 with up to 16
 // pairs as columns; more than 16 take the weights again, from the caches. Products are exact and sums fp32
@@ -55,8 +55,8 @@ PMN_DEV float dot2(uint32_t a, uint32_t b, float c)
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
 }
 
-// Byte `sel` of a code word as two bf16
-#define PMN_FP4_TO_BF16(w, sel) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((w), 1.0f, (sel)))
+// Byte `sel` of a code word, times a power of two, as two bf16
+#define PMN_FP4_TO_BF16(w, two, sel) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((w), (two), (sel)))
 
 // 8 codes times their scale d as bf16
 PMN_DEV bf16x8 gemv_values(uint32_t codes, float d)
@@ -271,15 +271,20 @@ __global__ __launch_bounds__(W * 64, 4) void k_gemv(GemvArgs p, int pitch, int l
                                 x[c][q] = *reinterpret_cast<const uint4*>(xs + c * xrow + u * 256 + g * 64 + h * 32 + q * 16);
 #pragma unroll
                         for (int t = 0; t < RT; t++) {
+                            // d16 = 2 two m: its power of two goes with the codes, so that the sum of 16 is no
+                            // larger than the block's share of the result (with plain codes it passed fp32's range
+                            // at |x| from 2^121 on), and 1/2 <= m < 1 with the sum, zero with a scale of zero
                             const float d16 = e4m3_value((s[t] >> (8 * h)) & 0xFFu);
+                            const float two = __uint_as_float(__float_as_uint(d16) & 0x7F800000u);
+                            const float m = __builtin_amdgcn_frexp_mantf(d16);
                             uint32_t v[8];
 #pragma unroll
                             for (int q = 0; q < 2; q++) {
                                 const uint32_t w = b.c[t][2 * h + q];
-                                v[4 * q] = PMN_FP4_TO_BF16(w, 0);
-                                v[4 * q + 1] = PMN_FP4_TO_BF16(w, 1);
-                                v[4 * q + 2] = PMN_FP4_TO_BF16(w, 2);
-                                v[4 * q + 3] = PMN_FP4_TO_BF16(w, 3);
+                                v[4 * q] = PMN_FP4_TO_BF16(w, two, 0);
+                                v[4 * q + 1] = PMN_FP4_TO_BF16(w, two, 1);
+                                v[4 * q + 2] = PMN_FP4_TO_BF16(w, two, 2);
+                                v[4 * q + 3] = PMN_FP4_TO_BF16(w, two, 3);
                             }
 #pragma unroll
                             for (int c = 0; c < C; c++) {
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(W * 64, 4) void k_gemv(GemvArgs p, int pitch, int l
                                     sum = dot2(v[4 * q + 2], x[c][q].z, sum);
                                     sum = dot2(v[4 * q + 3], x[c][q].w, sum);
                                 }
-                                acc[c][t] = __builtin_fmaf(sum, d16, acc[c][t]);
+                                acc[c][t] = __builtin_fmaf(sum, m, acc[c][t]);
                             }
                         }
                     }
@@ -300,7 +305,7 @@ __global__ __launch_bounds__(W * 64, 4) void k_gemv(GemvArgs p, int pitch, int l
             for (int c = 0; c < C; c++)
 #pragma unroll
                 for (int t = 0; t < RT; t++) {
-                    float v = acc[c][t];
+                    float v = acc[c][t] * 2.0f;
                     v += __shfl_xor(v, 16, 64);
                     v += __shfl_xor(v, 32, 64);
                     acc[c][t] = v;
