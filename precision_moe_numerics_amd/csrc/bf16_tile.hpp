@@ -13,11 +13,12 @@
 // fragments of stage v + 1 while the MFMAs of stage v run from registers. Bounds are the buffer
 // descriptor's: rows and k past the operand read as zeros, so every size that is a multiple of 8 runs
 // the same code.
-//   KC stage: rows of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r / 4) % 4): a quarter
-//     wavefront's ds_read_b128 covers all 64 banks (248 B/clk/CU measured). In the tiles with PAIRS, where
-//     both operands are KC or C alone is, two stages at a time: rows of 128 bytes, chunk c at slot
-//     c ^ ((r / 2) % 8), so that a load takes whole lines of 8 rows and not halves of 16 (49152 x 4096 x 7168,
-//     both KC: 2130 us with halves, 2025 so; 65536 x 7168 x 2048 in 48 groups, C alone: 1866 and 1770).
+//   KC stage: in the tiles with PAIRS, where both operands are KC or C alone is, two stages at a time: rows
+//     of 128 bytes, 16-byte chunk c of row r at slot c ^ ((r / 2) % 8), so that a load takes whole lines of 8
+//     rows and not halves of 16 (49152 x 4096 x 7168, both KC: 2130 us with halves, 2025 so; 65536 x 7168 x 2048
+//     in 48 groups, C alone: 1866 and 1770). In the others (a split contraction's short parts) single stages:
+//     rows of 64 bytes, chunk c at slot c ^ ((r / 4) % 4): a quarter wavefront's ds_read_b128 covers all 64
+//     banks (248 B/clk/CU measured).
 //   RC stage: 32 stored rows (k) of the tile's width, read by ds_read_b64_tr_b16, which hands lane i
 //     of 16 the column i of 4 k; the 32-byte pairs of chunks of row k are permuted by
 //     ((k / 8) % 2) | 2 (k % 4), so that the 4 k of 16 lanes lie in different banks (174 B/clk/CU
@@ -151,7 +152,7 @@ static __device__ const uint4 ffn_zeros = {0u, 0u, 0u, 0u};   // what a gathered
 
 // WR x WC wavefronts, each RB x CB blocks of 32 x 32; a ring of NST stages, or of two and a half or three pairs
 // of them (PAIRS, where both operands are k-contiguous; where C alone is, NST stages of R and three pairs of C)
-template <int WR_, int WC_, int RB_, int CB_, int NST_>
+template <int WR_, int WC_, int RB_, int CB_, int NST_, bool PAIRS_ = true>
 struct FfnTile {
     static constexpr int WR = WR_, WC = WC_, RB = RB_, CB = CB_, NST = NST_;
     static constexpr int BR = WR * RB * 32, BC = WC * CB * 32;
@@ -161,11 +162,12 @@ struct FfnTile {
     static constexpr int OPITCH = BR + 4;                       // floats per staged output row
     static constexpr int OROWS = WC * 32;                       // output rows staged at a time
     static constexpr bool HALVES = RB_ * CB_ == 16;
-    typedef FfnTile<WR_, WC_, RB_, CB_ / 2, NST_> Half;         // of the output rows, all of the columns
-    static constexpr bool PAIRS = RPW % 2 == 0;   // of stages, where an operand is k-contiguous
+    typedef FfnTile<WR_, WC_, RB_, CB_ / 2, NST_, PAIRS_> Half;   // of the output rows, all of the columns
+    static constexpr bool PAIRS = PAIRS_;         // of stages, where an operand is k-contiguous
     static constexpr int RING = !PAIRS ? NST * STAGE : BR == BC ? 5 * BR * 128 : 3 * (BR + BC) * 128, OUTB = OROWS * OPITCH * 4;
     static constexpr int LDS = RING > OUTB ? RING : OUTB;
     static_assert(BR / 16 % (WR * WC) == 0 && BC / 16 % (WR * WC) == 0, "every wavefront loads the same pieces");
+    static_assert(!PAIRS || RPW % 2 == 0, "half of a pair's pieces of R in each step");
     static_assert((PAIRS ? 6 : NST - 1) * (PPW + 1) <= 63, "vmcnt");   // loads on their way before the first wait
 };
 

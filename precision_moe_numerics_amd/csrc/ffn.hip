@@ -199,6 +199,7 @@ __global__ __launch_bounds__(512, 2) void k_ffn_few(FfnArgs p)
 typedef FfnTile<2, 2, 4, 4, 4> FfnLarge;    // 256 x 256, one workgroup per CU
 typedef FfnTile<2, 2, 2, 2, 4> FfnMid;      // 128 x 128
 typedef FfnTile<4, 1, 1, 2, 4> FfnFew;      // 128 x 64: few output rows, the R operand streams
+typedef FfnTile<4, 1, 1, 2, 4, false> FfnShort;   // the same by single stages
 
 constexpr int FFN_CUS = 256;   // the split's target; fixed, so that results depend on the sizes alone
 
@@ -235,6 +236,18 @@ static FfnPlan ffn_plan(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
     if (t >= FFN_CUS || stages < 32) return {1, 0};
     const int s = split_for(t, 16);
     return {1, s > 1 ? s : 0};
+}
+
+// Whether the 128 x 64 tiles load their part of the contraction by pairs of stages: where it is long enough for
+// the pairs' prologue of five stages and, with k-contiguous weights, all parts begin on a whole line. (One product,
+// contraction x columns, us by pairs / single stages: 17 tokens, 4096 x 2048 in parts of 8 stages, 6.7 / 6.5; 128 tokens,
+// 7168 x 4096 in parts of 56, 18.7 / 21.9; 300 tokens, 7168 x 2048 in parts of 74 and 75, 21.5 / 19.4. Parts of 10 to
+// 14 stages between 4% faster and 9% slower by pairs. Row-contiguous weights in parts of 74 and 75, the whole data
+// gradient of 300 tokens through a block of 7168 x 2048: 60.6 / 61.4.)
+static bool ffn_by_pairs(int64_t K, int splits, bool rkc)
+{
+    const int64_t stages = (K + 31) / 32;
+    return stages >= 16 * splits && (!rkc || splits == 1 || stages % (2 * splits) == 0);
 }
 
 static int64_t ffn_part_floats(int64_t Nc, int64_t Nr, int64_t K, bool ckc)
@@ -309,7 +322,10 @@ static void ffn_gemm(FfnArgs p, float* part, hipStream_t stream)
         return;
     }
     if (pl.tile == 1) ffn_launch_tile<FfnMid, RKC, CKC, FFN_PART>(p, stream);
-    else if constexpr (CKC) ffn_launch_tile<FfnFew, RKC, CKC, FFN_PART>(p, stream);
+    else if constexpr (CKC) {
+        if (ffn_by_pairs(p.K, pl.splits, RKC)) ffn_launch_tile<FfnFew, RKC, CKC, FFN_PART>(p, stream);
+        else ffn_launch_tile<FfnShort, RKC, CKC, FFN_PART>(p, stream);
+    }
     const int64_t n = p.Nc * ((EPI == FFN_SWIGLU ? p.F : p.Nr) / 8);
     hipLaunchKernelGGL((k_ffn_reduce<EPI>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, p);
 }
