@@ -587,7 +587,7 @@ int moe_grouped_gemm_fwd_bf16(const void* x, int64_t x_rows, const int32_t* gath
 {
     if (epilogue != PMN_EPI_F32 && epilogue != PMN_EPI_BF16 && epilogue != PMN_EPI_SWIGLU) return PMN_EINVAL;
     if (bad_group_shape(M, G, N, K, x_rows, gather != nullptr) || (epilogue == PMN_EPI_SWIGLU && N % 16 != 0) ||
-        !pmn::group_bf16_fits(M, G, N, K, true))
+        !pmn::group_rows_fit(M, G, N, K, true))
         return PMN_ESHAPE;
     if (M == 0) return PMN_OK;
     if (!x || !w || !offsets || !out) return PMN_EINVAL;
@@ -616,7 +616,7 @@ int moe_grouped_gemm_bwd_bf16(const void* dy, const void* x, int64_t x_rows, con
         (h13 && (gather || !dgrad)))
         return PMN_EINVAL;
     if (bad_group_shape(M, G, N, K, wgrad && x ? x_rows : M, gather != nullptr) ||
-        !pmn::group_bf16_fits(M, G, N, K, false))
+        (dgrad && !pmn::group_rows_fit(M, G, N, K, false)) || (wgrad && !pmn::group_wgrad_fits(M, G, N, K)))
         return PMN_ESHAPE;
     const bool rebuild = wgrad && !x && h13;
     if (!offsets || (wgrad && !db)) return PMN_EINVAL;

@@ -346,14 +346,20 @@ static int64_t wgrad_grid(int G, int64_t N, int64_t K, int64_t b)
     return (((N + b - 1) / b) * ((K + b - 1) / b) + 7) / 8 * 8 * G;
 }
 
-// A launch has fewer than 2^32 threads. fwd: the products with k-contiguous weights.
-bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd)
+// A launch has fewer than 2^32 threads.
+constexpr int64_t MOST_THREADS = ((int64_t)1 << 32) - 1;
+
+// The forward's launch, or dgrad's
+bool group_rows_fit(int64_t M, int G, int64_t N, int64_t K, bool fwd)
 {
-    const int64_t most = ((int64_t)1 << 32) - 1;
     const GroupTile& t = GROUP_TILES[group_plan(M, G, fwd ? N : K, fwd ? K : N, fwd)];
     // (SwiGLU's F features in tiles of half as many are at most one tile of R more)
-    if (group_grid(M, G, fwd ? N : K, t.br, t.bc) + (M / t.bc + G) > most / (t.bc == 16 ? 512 : 256)) return false;
-    return fwd || wgrad_grid(G, N, K, wgrad_large(M, G, N, K) ? 256 : 128) <= most / 256;
+    return group_grid(M, G, fwd ? N : K, t.br, t.bc) + (M / t.bc + G) <= MOST_THREADS / (t.bc == 16 ? 512 : 256);
+}
+
+bool group_wgrad_fits(int64_t M, int G, int64_t N, int64_t K)
+{
+    return wgrad_grid(G, N, K, wgrad_large(M, G, N, K) ? 256 : 128) <= MOST_THREADS / 256;
 }
 
 template <typename T, bool RKC, int EPI, bool GATHER>

@@ -164,8 +164,9 @@ hipError_t launch_ffn_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t*
 
 // ---- the expert layer on unquantized activations ----------------------------------------------
 
-// Whether the launches of these sizes are within what a launch holds (fwd: the forward's, else the backward's)
-bool group_bf16_fits(int64_t M, int G, int64_t N, int64_t K, bool fwd);
+// Whether these sizes are within what a launch holds: the forward's or dgrad's, and wgrad's
+bool group_rows_fit(int64_t M, int G, int64_t N, int64_t K, bool fwd);
+bool group_wgrad_fits(int64_t M, int G, int64_t N, int64_t K);
 hipError_t launch_group_fwd_bf16(const uint16_t* x, const int32_t* gather, const uint16_t* w, const int64_t* offsets,
                                  int G, int64_t M, int64_t N, int64_t K, int epilogue, void* out, uint16_t* h13,
                                  hipStream_t stream);
