@@ -641,7 +641,7 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise PmnError(f"{name} must be on the GPU")
-    current = torch._C._cuda_getDevice()   # torch.cuda.current_device() without its check that CUDA is up: t is on it
+    current = torch.cuda.current_device()
     if dev != current:
         raise PmnError(f"{name} is on cuda:{dev}, the current device is cuda:{current}")
     return dev
