@@ -809,7 +809,7 @@ def swiglu_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
 
 # ---- the expert layer on unquantized activations --------------------------------------------
 
-def _group_args(w: torch.Tensor, offsets: torch.Tensor, M: int, N: int, gather, what: str, src_rows: int):
+def _group_args(w: torch.Tensor, offsets: torch.Tensor, M: int, N: int, gather, what: str, src_rows: Optional[int]):
     """(G, K) of bf16 weights [G*N, K]."""
     _need(offsets is not None and offsets.dtype == torch.int64 and offsets.dim() == 1 and offsets.numel() >= 2,
           "offsets must be int64 [G+1]")
@@ -817,7 +817,10 @@ def _group_args(w: torch.Tensor, offsets: torch.Tensor, M: int, N: int, gather, 
     if w.dtype != torch.bfloat16 or w.dim() != 2 or w.shape[0] != G * N:
         raise PmnError(f"w must be bf16 [G*N, K] with {G * N} rows")
     _index(gather, M, torch.int32, "gather")
-    _debug_indices(what, offsets, M, gather, src_rows)
+    if src_rows is None:   # no rows that gather would name
+        _debug_indices(what, offsets, M)
+    else:
+        _debug_indices(what, offsets, M, gather, src_rows)
     return G, w.shape[1]
 
 
@@ -868,7 +871,7 @@ def moe_grouped_gemm_bwd_bf16(dy: torch.Tensor, x: Optional[torch.Tensor], w: to
     _need(dgrad or da is None, "da needs BWD_DGRAD")
     _need(wgrad or db is None, "db needs BWD_WGRAD")
     _need(x is not None or not wgrad or h13 is not None, "the weight gradient needs x or h13")
-    G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_bwd_bf16", 0 if x is None else x.shape[0])
+    G, K = _group_args(w, offsets, M, N, gather, "moe_grouped_gemm_bwd_bf16", None if x is None else x.shape[0])
     if x is not None:
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
             raise PmnError(f"x must be bf16 [rows, {K}]")
